@@ -543,6 +543,169 @@ ri_status ri_gather_blocks_shaped(const ri_gather_buffers* bufs, const ri_copy_d
 ri_status ri_gather_shape(int64_t host_copies, int64_t total_copies, int32_t* threads,
                           int32_t* blocks_per_sm);
 
+/* ---- Exact token cache ------------------------------------------------
+ * The pages' wave index approximates a long context; its inputs arrive
+ * rotary-encoded and every sequence has an index of its own.  The calls below
+ * are for what stands beside it: rotary positions (for the index build's
+ * keys, the append's and the queries as well), and a cache of exact tokens
+ * per (sequence, KV head) which a batch reads together with one shared
+ * prefix, and which gives up its least-attended tokens under a budget.  The
+ * pages have no counterpart of these calls. */
+
+/* A strided tensor of heads [B][T][heads][head_dim], head_dim contiguous;
+ * strides in elements (any sign of layout: a slice of a projection's output,
+ * or the transpose of [B][heads][T][head_dim]). */
+typedef struct {
+  void* data;
+  int64_t stride_b, stride_t, stride_h;
+} ri_heads;
+
+enum { RI_BF16 = 0, RI_FP16 = 1, RI_FP32 = 2 };
+
+/* Scalings of the rotary frequencies f_i = base^(-2i / rotary_dim):
+ *  RI_ROPE_NONE    as they are
+ *  RI_ROPE_LINEAR  f_i / factor
+ *  RI_ROPE_NTK     base' = base * factor^(n / (n - 2)), n = rotary_dim
+ *  RI_ROPE_BANDS   t f_i + (1 - t) f_i / factor with t = (original_len f_i /
+ *                  2 pi - low) / (high - low) clamped to [0, 1]
+ *  RI_ROPE_YARN    r f_i / factor + (1 - r) f_i, r the ramp over i from
+ *                  floor(c(high)) to ceil(c(low)), c(t) = n ln(original_len /
+ *                  (2 pi t)) / (2 ln base); the rotated values are scaled by
+ *                  0.1 ln(factor) + 1 (1 for factor <= 1)                   */
+enum { RI_ROPE_NONE = 0, RI_ROPE_LINEAR = 1, RI_ROPE_NTK = 2, RI_ROPE_BANDS = 3,
+       RI_ROPE_YARN = 4 };
+typedef struct {
+  int32_t rotary_dim;   /* rotated elements of a head: even, 2..256       */
+  int32_t scaling;      /* RI_ROPE_*                                      */
+  int32_t original_len; /* BANDS, YARN: trained length, >= 1              */
+  int32_t reserved;     /* 0                                              */
+  double base;          /* > 1                                            */
+  double factor;        /* > 0 (ignored by NONE)                          */
+  double low, high;     /* BANDS, YARN: turns over original_len, 0 < low <
+                           high                                           */
+} ri_rotary_config;
+
+/* Fills turns[rotary_dim / 2] (host): every pair's turns per position as a
+ * 64-bit fraction (round(f / 2 pi * 2^64)), so that position * turns modulo
+ * 2^64 is the angle's fraction of a turn without rounding at any position.
+ * frequencies: optional double[rotary_dim / 2], the f themselves; magnitude:
+ * the factor on the rotated values.  Host only. */
+ri_status ri_rotary_table(const ri_rotary_config* cfg, uint64_t* turns, double* frequencies,
+                          double* magnitude);
+
+/* A table on the device, as the rotating calls take it. */
+typedef struct {
+  const uint64_t* turns; /* device [rotary_dim / 2], 8-byte aligned        */
+  int32_t rotary_dim;    /* even, 2 <= rotary_dim <= head_dim              */
+  int32_t interleaved;   /* 0: pairs (i, i + rotary_dim / 2); 1: (2i, 2i+1) */
+  float magnitude;
+} ri_rope;
+
+/* Rotary positions: for every pair (a, b) of the first rotary_dim elements
+ * of each head, (a c - b s, b c + a s) with c, s = magnitude * cos, sin of
+ * position * f; the other elements are copied.  Computed in fp32 and rounded
+ * once to the dtype (RI_BF16, RI_FP16 or RI_FP32) of x and out.
+ * x, out   [batch][tokens][heads][head_dim], strided; out may be x itself
+ *          (same data and strides), otherwise the two must not overlap.
+ *          head_dim 2..256; data aligned to the element.  16-byte aligned
+ *          rows with rotary_dim / 2 elements of a multiple of 16 bytes (half
+ *          layout; rotary_dim elements when interleaved) take the vector
+ *          path, others an element-wise one.
+ * pos      int32 [batch][tokens], tokens contiguous, pos_stride elements
+ *          between sequences (0: one row for all); any value, negative ones
+ *          turn backwards.
+ * inverse  nonzero: the angle's sign is turned, (a c + b s, b c - a s): the
+ *          transpose, which is the backward pass of the rotation. */
+ri_status ri_rotary(int32_t batch, int32_t tokens, int32_t heads, int32_t head_dim,
+                    int32_t dtype, const ri_heads* x, const int32_t* pos, int64_t pos_stride,
+                    const ri_rope* rope, const ri_heads* out, int32_t inverse,
+                    ri_stream_t stream);
+
+/* The cache of exact tokens of every (sequence, KV head).  Caller-owned
+ * device memory; a token's slot is its row.
+ *  K, V    bf16 [B][H_kv][capacity][128]
+ *  pos     int32 [B][H_kv][capacity]   positions of the stored tokens
+ *  weight  fp32 [B][H_kv][capacity]    attention weight each has gathered
+ *  lens    int32 [B][H_kv]             stored tokens, in rows 0 .. lens - 1
+ * Rows from lens on are never read, and are written by ri_token_append only.
+ * A length outside [0, capacity] is recorded as RI_ERR_INVALID_ARG in the
+ * status word of the call's workspace and taken as the nearer bound. */
+typedef struct {
+  int32_t batch, num_kv_heads, group_size, head_dim, capacity;
+  void* K;
+  void* V;
+  int32_t* pos;
+  float* weight;
+  int32_t* lens;
+} ri_token_cache;
+
+/* Stores `tokens` new tokens of every sequence behind its last one, keys
+ * rotated by rope (NULL: stored as they are), with weight 0, and rotates the
+ * step's queries beside them.
+ * k, v     bf16 [B][tokens][H_kv][128], strided; 16-byte aligned rows.
+ * q        optional bf16 [B][tokens][H_kv G][128], strided, rotated into
+ * q_out    bf16 [B][tokens][H_kv G][128], dense.
+ * pos      as for ri_rotary.
+ * lens_out int32 [B][H_kv]: the lengths after the call; cache->lens itself
+ *          to advance them in place (another array leaves cache->lens as it
+ *          was, so that a draft can be taken back).
+ * workspace >= 256 device bytes (status word).  A (sequence, head) without
+ * room for all the tokens stores none, keeps its length, and
+ * RI_ERR_CAPACITY is recorded. */
+ri_status ri_token_append(const ri_token_cache* cache, int32_t tokens, const ri_heads* k,
+                          const ri_heads* v, const int32_t* pos, int64_t pos_stride,
+                          const ri_rope* rope, const ri_heads* q, void* q_out,
+                          int32_t* lens_out, void* workspace, ri_stream_t stream);
+
+/* Tokens that every sequence of a batch shares: bf16 [H_kv][length][128],
+ * 128 contiguous, strides in elements (multiples of 8, or a single row). */
+typedef struct {
+  const void* K;
+  const void* V;
+  int32_t length;
+  int32_t reserved;          /* 0 */
+  int64_t stride_t, stride_h; /* of K and of V */
+} ri_token_prefix;
+
+/* Bytes of workspace ri_token_attend needs (0 on an invalid argument). */
+size_t ri_token_attend_workspace(const ri_token_cache* cache, int32_t prefix_len);
+
+/* Attention of one query token per sequence over the shared prefix and the
+ * sequence's own cached tokens:
+ *  out_h = sum_i p_i v_i, p = softmax(q_h . k_i / sqrt(128)) over both;
+ *  weight[b][h_kv][i] += sum of p_i over the head's G query heads, for the
+ *  own tokens, when add_weight is nonzero.
+ * The prefix is read once for the whole batch.
+ * q, out   bf16 [B][H_kv G][128];  lse  optional fp32 [B][H_kv G].
+ * prefix   NULL or length 0: none.  A row with nothing to attend to gives
+ *          out = 0 and lse = -inf. */
+ri_status ri_token_attend(const ri_token_cache* cache, const void* q,
+                          const ri_token_prefix* prefix, void* out, float* lse,
+                          int32_t add_weight, void* workspace, size_t workspace_bytes,
+                          ri_stream_t stream);
+
+/* Bytes of workspace ri_token_evict needs (0 on an invalid argument). */
+size_t ri_token_evict_workspace(const ri_token_cache* cache, int32_t budget);
+
+/* Reduces every (sequence, KV head) to keep = min(lens, budget) tokens: first
+ * those at positions < keep_first and those at positions > newest -
+ * keep_recent (newest: the largest stored position), then the ones of
+ * largest weight, ties to the lower row; a NaN weight counts as -inf.  Kept
+ * tokens in rows below `keep` stay there; the kept tokens behind fill the
+ * rows of the dropped ones, both in row order.  The rows' order is not their
+ * positions' order afterwards, which attention does not see.
+ * out      the cache that receives the result: `cache` itself (in place), or
+ *          one of equal batch and head counts and capacity >= min(budget,
+ *          cache capacity).  Each of its arrays may also be the source's own
+ *          (K and V in place, lengths and weights kept elsewhere, say); one
+ *          that is shared must have the same capacity, others must not
+ *          overlap.  Rows from the new length on are left as they were.
+ * budget >= 1, keep_first >= 0, keep_recent >= 0, keep_first + keep_recent
+ * <= budget. */
+ri_status ri_token_evict(const ri_token_cache* cache, int32_t budget, int32_t keep_first,
+                         int32_t keep_recent, const ri_token_cache* out, void* workspace,
+                         size_t workspace_bytes, ri_stream_t stream);
+
 /* Synchronises `stream` and returns the status word previous calls wrote
  * into `workspace` (RI_OK if no device-side failure was recorded); a failure
  * read is cleared, so the next read reports only later failures. */

@@ -21,11 +21,20 @@ _EXPORTS = (
     "Decoder", "index_open", "index_append", "index_append_workspace_bytes",
     "gather_shape")
 
-__all__ = list(_EXPORTS)
+# rotary positions and the exact token cache
+_TOKEN_EXPORTS = (
+    "ROPE_SCALINGS", "RotaryConfig", "RotaryTable", "TokenCache", "rotary", "token_append",
+    "token_attend", "token_attend_workspace_bytes", "token_evict",
+    "token_evict_workspace_bytes")
+
+__all__ = list(_EXPORTS + _TOKEN_EXPORTS)
 
 
 def __getattr__(name):
     if name in _EXPORTS:
         binding = importlib.import_module("._binding", __name__)
         return getattr(binding, name)
+    if name in _TOKEN_EXPORTS:
+        tokens = importlib.import_module("._tokens", __name__)
+        return getattr(tokens, name)
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

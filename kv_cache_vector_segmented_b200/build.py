@@ -13,7 +13,8 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libretroinfer.so")
 SOURCES = ["api.cpp", "cache.cpp", "decode.cu", "gather.cu", "grow.cu", "kmeans.cu",
-           "static_scratch.cu"]
+           "rotary.cu", "static_scratch.cu", "token_api.cpp", "token_attend.cu",
+           "token_evict.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 

@@ -55,9 +55,6 @@ cudaError_t set_smem_once(int slot, const void* func, int bytes) {
   return e;
 }
 
-static bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-static bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
-
 bool make_geometry(const ri_index_config* cfg, Geometry* g) {
   if (!cfg) {
     set_error("config is NULL");
@@ -278,19 +275,6 @@ bool make_append_layout(const Geometry& g, const ri_index_config* cfg, AppendLay
 }  // namespace ri
 
 using namespace ri;
-
-#define RI_CHECK(cond, code, ...) \
-  do {                            \
-    if (!(cond)) {                \
-      set_error(__VA_ARGS__);     \
-      return code;                \
-    }                             \
-  } while (0)
-
-static ri_status cuda_fail(cudaError_t e, const char* what) {
-  set_error("%s: %s", what, cudaGetErrorString(e));
-  return RI_ERR_CUDA;
-}
 
 namespace ri {
 ri_status check_gather_buffers(const ri_gather_buffers* bufs) {

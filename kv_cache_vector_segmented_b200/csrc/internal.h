@@ -192,8 +192,69 @@ cudaError_t launch_close_gather(const Geometry& g, const ri_index& idx, void* sK
 cudaError_t launch_close_scatter(const Geometry& g, const ri_index& idx, const ri_index& seg,
                                  cudaStream_t s);
 
+// --------------------------------------------------------------- token cache
+// Strided rows of heads on the device (ri_heads) and the rotation of a pair
+// (ri_rope) are passed to the kernels as given.
+struct RotaryArgs {
+  int B, T, heads, d;
+  ri_heads x, out;
+  const int32_t* pos;
+  long long pos_stride;  // elements between the positions of two sequences
+  ri_rope rope;
+  bool inverse;
+};
+cudaError_t launch_rotary(const RotaryArgs& a, int dtype, cudaStream_t s);
+
+struct AppendTokensArgs {
+  ri_token_cache c;
+  int T;
+  ri_heads q, k, v;      // q.data NULL: no query heads
+  void* q_out;           // bf16 [B][T][H G][d]
+  const int32_t* pos;
+  long long pos_stride;
+  ri_rope rope;          // turns NULL: no rotation
+  int32_t* lens_out;
+  int* status;
+};
+cudaError_t launch_token_append(const AppendTokensArgs& a, cudaStream_t s);
+
+struct TokenAttendArgs {
+  ri_token_cache c;
+  ri_token_prefix p;     // length 0: none
+  const void* q;
+  void* out;
+  float* lse;
+  bool add_weight;
+  char* ws;
+};
+// Workspace of ri_token_attend in bytes.
+size_t token_attend_bytes(const ri_token_cache& c, int prefix_len);
+cudaError_t launch_token_attend(const TokenAttendArgs& a, cudaStream_t s);
+
+struct TokenEvictArgs {
+  ri_token_cache c, out;
+  int budget, keep_first, keep_recent;
+  char* ws;
+};
+size_t token_evict_bytes(const ri_token_cache& c, int budget);
+cudaError_t launch_token_evict(const TokenEvictArgs& a, cudaStream_t s);
+
 // Thread-local last error.
 void set_error(const char* fmt, ...);
+// Argument checks of the entry points: a failed one sets the last error.
+#define RI_CHECK(cond, code, ...) \
+  do {                            \
+    if (!(cond)) {                \
+      set_error(__VA_ARGS__);     \
+      return code;                \
+    }                             \
+  } while (0)
+inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+inline ri_status cuda_fail(cudaError_t e, const char* what) {
+  set_error("%s: %s", what, cudaGetErrorString(e));
+  return RI_ERR_CUDA;
+}
 int num_sms();
 // Raises a kernel's dynamic shared memory limit once per device (outside any
 // stream capture after the first call on that device).  `slot` names the
