@@ -1,11 +1,23 @@
 // Attention of one token per sequence over a shared prefix and the sequence's
-// own cached tokens (ri_token_attend).
+// own cached tokens (ri_token_attend): three launches.
 //
-// Split softmax: every block takes a share of one (sequence, KV head)'s
-// tokens (prefix first, then own) and leaves (maximum, sum, weighted value
-// sum) per query head; a second launch merges the shares by log-sum-exp,
-// writes out and lse, and adds the own tokens' probabilities to their
-// weights from the scores kept by the first.
+//  prefix_kernel  all query rows of a KV head against the head's prefix, on
+//                 the 5th-generation tensor cores (the batch's rows make one
+//                 tall matrix, so the prefix is read once for all of them);
+//  own_kernel     each (sequence, KV head)'s G rows against its own tokens,
+//                 on warp-level tensor-core tiles (8 rows do not fill a tall
+//                 tile); keeps the scores when weights are to be added;
+//  merge_kernel   joins the shares by log-sum-exp, writes out and lse, and
+//                 adds the own tokens' probabilities to their weights.
+//
+// Every share is (reference m, sum l, numerator) in units of log2:
+//   l = sum_i 2^(s_i - m),  num = sum_i 2^(s_i - m) v_i,  s = q.k log2(e)/sqrt(d),
+// the merge takes M = max m, l = sum 2^(m - M) l, num likewise.  Scores, sums
+// and numerators are fp32; only the probabilities enter the value product as
+// bf16 (half a step, 2^-8, relative, against the output's own 2^-8), the sum
+// l is taken of the unrounded ones.
+#include <string.h>
+
 #include "common.cuh"
 #include "internal.h"
 
@@ -13,201 +25,940 @@ namespace ri {
 
 namespace {
 
-constexpr int kThreads = 128;
-constexpr int kWarps = 4;
-constexpr float kScale = 0.08838834764831845f;  // 1 / sqrt(128)
+constexpr float kScaleLog2 = 0.08838834764831845f * 1.4426950408889634f;  // log2(e) / sqrt(128)
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kD = kHeadDim;
+constexpr int kTile = 128;                  // query rows, keys of a tile
+constexpr int kTileBytes = kTile * kD * 2;  // 32 KB of bf16
+constexpr int kHalfTile = kTileBytes / 2;   // 64 of the 128 columns, 128-byte rows
 
-struct AttendLayout {
-  int splits;
-  size_t off_ml, off_num, off_score, total;
+// ---------------------------------------------------------------- work split
+// The prefix is cut into tiles of 128 keys, the query rows of a KV head
+// (b, g in order) into tiles of 128.  A unit is a KV head and two row tiles
+// that share each key tile from shared memory (the last unit of an odd count
+// has one); its work is 2 (or 1) per key tile.  Block c takes the work from
+// total * c / blocks to total * (c + 1) / blocks of all units in a row, so
+// every block carries the same share to within a tile, whatever the lengths.
+// Block c's share of unit u lies in slots 2 (c + u) and 2 (c + u) + 1, which
+// no other (c, u) has, as u grows with c.
+struct PrefixPlan {
+  int rows;            // B * G, rows per KV head
+  int tiles;           // row tiles per KV head
+  int per_head;        // units per KV head
+  int units;           // over all KV heads
+  int key_tiles;
+  int blocks;
+  long long head_work, total;  // work per KV head, in all
+  __host__ __device__ int work_per_tile(int u) const {
+    return (u % per_head) * 2 + 1 < tiles ? 2 : 1;
+  }
+  __host__ __device__ long long start(int u) const {
+    return (u / per_head) * head_work + (long long)(u % per_head) * 2 * key_tiles;
+  }
+  __host__ __device__ int tile_at(int u, long long x) const {  // first key tile at or past x
+    const long long s = x - start(u);
+    if (s <= 0) return 0;
+    const int w = work_per_tile(u);
+    const long long t = (s + w - 1) >> (w - 1);
+    return t < key_tiles ? (int)t : key_tiles;
+  }
+  __host__ __device__ long long from(int c) const { return total * c / blocks; }
+  __host__ __device__ int unit_of(long long x) const {  // the unit holding work x
+    const int h = (int)(x / head_work);
+    const int i = (int)((x - h * head_work) / (2ll * key_tiles));
+    return h * per_head + (i < per_head ? i : per_head - 1);
+  }
 };
 
-AttendLayout layout(const ri_token_cache& c, int prefix_len) {
+PrefixPlan plan_prefix(const ri_token_cache& c, int prefix_len) {
+  PrefixPlan p = {};
+  p.rows = c.batch * c.group_size;
+  p.tiles = (p.rows + kTile - 1) / kTile;
+  p.per_head = (p.tiles + 1) / 2;
+  p.units = c.num_kv_heads * p.per_head;
+  p.key_tiles = (prefix_len + kTile - 1) / kTile;
+  p.head_work = (long long)p.tiles * p.key_tiles;
+  p.total = p.head_work * c.num_kv_heads;
+  const long long pieces = (long long)p.units * p.key_tiles;
+  const int sms = num_sms();
+  p.blocks = (int)(pieces < sms ? pieces : sms);
+  return p;
+}
+
+struct AttendLayout {
+  int splits;  // shares of a (sequence, KV head)'s own tokens
+  // prefix shares: ml fp32 [slots][128][2], num fp32 [slots][32][128][4] (four
+  // columns of every row, so that a warp's rows store 512 contiguous bytes);
+  // own shares: ml [units][splits][G][2], num [units][splits][G][128];
+  // score fp32 [units][capacity][Gp], Gp = 4 or 8
+  size_t off_pml, off_pnum, off_ml, off_num, off_score, total;
+};
+
+AttendLayout layout(const ri_token_cache& c, const PrefixPlan& pp) {
   AttendLayout L;
   const size_t units = (size_t)c.batch * c.num_kv_heads;
-  const long long tokens = (long long)prefix_len + c.capacity;
-  long long splits = (1184 + units - 1) / units;
-  if (splits > (tokens + 63) / 64) splits = (tokens + 63) / 64;
-  if (splits < 1) splits = 1;
+  // own shares: four blocks per SM in all, none of fewer than 64 tokens
+  long long splits = (4 * 148 + units - 1) / units;
+  const long long most = (c.capacity + 63) / 64;
+  if (splits > most) splits = most;
   L.splits = (int)splits;
+  const size_t slots = pp.blocks ? 2 * (size_t)(pp.blocks + pp.units) : 0;
   size_t off = kStatusBytesHost;
+  L.off_pml = off;
+  off = align_up(off + slots * kTile * 2 * sizeof(float), 256);
+  L.off_pnum = off;
+  off = align_up(off + slots * kTile * kD * sizeof(float), 256);
   L.off_ml = off;
   off = align_up(off + units * splits * c.group_size * 2 * sizeof(float), 256);
   L.off_num = off;
-  off = align_up(off + units * splits * c.group_size * kHeadDim * sizeof(float), 256);
+  off = align_up(off + units * splits * c.group_size * kD * sizeof(float), 256);
   L.off_score = off;
-  off = align_up(off + units * c.capacity * c.group_size * sizeof(float), 256);
+  off = align_up(off + units * c.capacity * (c.group_size <= 4 ? 4 : 8) * sizeof(float), 256);
   L.total = off;
   return L;
 }
 
 struct AttendParams {
   ri_token_cache c;
-  ri_token_prefix p;
   const __nv_bfloat16* q;
   __nv_bfloat16* out;
   float* lse;
-  float* ml;     // [units][splits][G][2]
-  float* num;    // [units][splits][G][128]
-  float* score;  // [units][capacity][G]
+  float* pml;
+  float* pnum;
+  float* ml;
+  float* num;
+  float* score;
   int* status;
+  PrefixPlan plan;  // blocks == 0: no prefix
+  int prefix_len;
   int splits, add_weight;
 };
+
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+__device__ __forceinline__ void named_barrier(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
+// ------------------------------------------------------------ prefix kernel
+constexpr int kRing = 5;                  // K / V tiles in flight
+constexpr int kSoftmaxWarps = 8;          // two warpgroups, one per slot
+constexpr int kWarpMma = 8, kWarpLoad = 9;
+constexpr int kPrefixThreads = 384;       // warps 10 and 11 fill the third warpgroup
+// Registers: 168 per thread at launch (384 x 168 = 64512); the softmax
+// warpgroups hold a row's 128 scores and take 200 each, the third goes down
+// to 96: 256 x 200 + 128 x 96 = 63488.
+constexpr int kRegsSoftmax = 200, kRegsRest = 96;
+// TMEM columns: scores (and, over them, the probabilities) of slot i, then
+// the numerators
+constexpr uint32_t kColS = 0, kColO = 256;
+constexpr float kLazy = 8.f;  // log2: the reference moves when the maximum passes it by this
+
+struct PrefixShared {
+  uint64_t full[kRing], empty[kRing];
+  uint64_t q_full, s_full[2], p_full[2], o_full[2], drain;
+  uint32_t tmem;
+};
+constexpr size_t kPrefixSmem = 1024 + (2 + kRing) * (size_t)kTileBytes + sizeof(PrefixShared);
+
+// V tile [key][d] as the B operand of num += P V (N = d contiguous, "MN
+// major"): 128-byte swizzle, 64 columns of d per half tile; adjacent halves
+// kHalfTile apart (leading offset), adjacent groups of 8 keys 1024 bytes
+// apart (stride offset).
+__device__ __forceinline__ uint64_t umma_desc_v(uint32_t addr) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((addr >> 4) & 0x3FFF);
+  d |= static_cast<uint64_t>(kHalfTile >> 4) << 16;
+  d |= static_cast<uint64_t>(1024 >> 4) << 32;
+  d |= static_cast<uint64_t>(1) << 46;
+  d |= static_cast<uint64_t>(2) << 61;
+  return d;
+}
+
+// D[tmem] (+)= A[tmem] B[smem], A = probabilities, two bf16 per column.
+__device__ __forceinline__ void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                        uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, int x, int y, int z,
+                                            uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+      "%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+      "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+      "%14,%15}, [%16];\n tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+        "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+// A share of one unit: key tiles [t0, t1), one or two row tiles.  With two
+// row tiles ("pair") both slots see every key tile; with one, the slots take
+// the key tiles in turn, so that one's softmax runs beside the other's
+// products here too, and are joined at the end.
+struct Share {
+  int head, row0, t0, t1;
+  bool pair;
+};
+
+__device__ __forceinline__ Share share_of(const PrefixPlan& p, int u, long long x0, long long x1) {
+  Share s;
+  s.head = u / p.per_head;
+  s.row0 = (u % p.per_head) * 2 * kTile;
+  s.t0 = p.tile_at(u, x0);
+  s.t1 = p.tile_at(u, x1);
+  s.pair = p.work_per_tile(u) == 2;
+  return s;
+}
+
+__global__ void __launch_bounds__(kPrefixThreads, 1)
+    prefix_kernel(const __grid_constant__ CUtensorMap map_k,
+                  const __grid_constant__ CUtensorMap map_v,
+                  const __grid_constant__ AttendParams p) {
+  extern __shared__ uint8_t raw[];
+  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~1023ull);
+  uint8_t* sq = base;                       // 2 query tiles
+  uint8_t* ring = base + 2 * kTileBytes;    // kRing K / V tiles
+  PrefixShared* sh = reinterpret_cast<PrefixShared*>(ring + kRing * kTileBytes);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const PrefixPlan& plan = p.plan;
+
+  if (warp == kWarpMma) {
+    tmem_alloc(&sh->tmem, 512);
+    tmem_relinquish();
+  }
+  if (tid == 0) {
+    for (int i = 0; i < kRing; ++i) {
+      mbar_init(&sh->full[i], 1);
+      mbar_init(&sh->empty[i], 1);
+    }
+    mbar_init(&sh->q_full, kSoftmaxWarps * 32);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh->s_full[i], 1);
+      mbar_init(&sh->p_full[i], 4);
+      mbar_init(&sh->o_full[i], 1);
+    }
+    mbar_init(&sh->drain, 1);
+    fence_barrier_init();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh->tmem;
+
+  const long long x0 = plan.from(blockIdx.x), x1 = plan.from(blockIdx.x + 1);
+  const int u0 = plan.unit_of(x0);
+  const int last_tile = plan.key_tiles - 1;
+  // A wait that expires is recorded once; its role then runs on without
+  // waiting, copying or multiplying, so every loop and barrier still ends.
+  bool ok = true;
+
+  if (warp >= kSoftmaxWarps) {
+    // one instruction for the whole warpgroup
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
+    if (warp == kWarpLoad) {
+      // ------------------------------------------------------------- loads
+      if (lane == 0) {
+        int n = 0;  // tiles loaded
+        tma_prefetch_desc(&map_k);
+        tma_prefetch_desc(&map_v);
+        auto load = [&](const CUtensorMap* map, int t, int head) {
+          const int st = n % kRing;
+          if (ok && n >= kRing && !mbar_wait(&sh->empty[st], (uint32_t)((n / kRing - 1) & 1))) {
+            record_status(p.status, RI_ERR_TIMEOUT);
+            ok = false;
+          }
+          if (!ok) return;
+          uint8_t* dst = ring + st * kTileBytes;
+          mbar_arrive_expect_tx(&sh->full[st], kTileBytes);
+          tma_load_3d(dst, map, 0, t * kTile, head, &sh->full[st]);
+          tma_load_3d(dst + kHalfTile, map, 64, t * kTile, head, &sh->full[st]);
+          ++n;
+        };
+        for (int u = u0; u < plan.units && plan.start(u) < x1; ++u) {
+          const Share s = share_of(plan, u, x0, x1);
+          const int ahead = s.pair ? 1 : 2;  // key tiles before the first value tile
+          for (int t = s.t0; t < s.t1 && t < s.t0 + ahead; ++t) load(&map_k, t, s.head);
+          for (int t = s.t0; t < s.t1; ++t) {
+            load(&map_v, t, s.head);
+            if (t + ahead < s.t1) load(&map_k, t + ahead, s.head);
+          }
+        }
+        // every copy has landed before the block's shared memory goes away
+        for (int i = n > kRing ? n - kRing : 0; i < n; ++i)
+          if (!mbar_wait(&sh->full[i % kRing], (uint32_t)((i / kRing) & 1)))
+            record_status(p.status, RI_ERR_TIMEOUT);
+      }
+      __syncwarp();
+    } else if (warp == kWarpMma) {
+      // -------------------------------------------------------- MMA issuer
+      if (lane == 0) {
+        constexpr uint32_t idesc_s = umma_idesc_bf16_f32(kTile, kTile);
+        constexpr uint32_t idesc_o = umma_idesc_bf16_f32(kTile, kD) | (1u << 16);  // B: MN major
+        const uint32_t q_addr = smem_u32(sq), ring_addr = smem_u32(ring);
+        int n = 0;  // tiles consumed
+        uint32_t q_phase = 0, p_phases = 0;  // bit i of p_phases: slot i
+        auto wait = [&](uint64_t* bar, uint32_t parity) {
+          if (ok && !mbar_wait(bar, parity)) {
+            record_status(p.status, RI_ERR_TIMEOUT);
+            ok = false;
+          }
+        };
+        auto wait_tile = [&](int i) { wait(&sh->full[i % kRing], (uint32_t)((i / kRing) & 1)); };
+        // S[slot] = Q K^T for the tile in ring slot i % kRing
+        auto scores = [&](int slot, int qtile, int i) {
+          if (!ok) return;
+          tc_fence_after();
+          const uint32_t a = q_addr + qtile * kTileBytes;
+          const uint32_t b = ring_addr + (i % kRing) * kTileBytes;
+#pragma unroll 1
+          for (int k = 0; k < 8; ++k) {  // rolled: one thread issues, registers are short here
+            const uint32_t off = (k >> 2) * kHalfTile + (k & 3) * 32;
+            umma_bf16(tmem + kColS + slot * kTile, umma_desc_sw128(a + off),
+                      umma_desc_sw128(b + off), idesc_s, k > 0);
+          }
+          umma_commit(&sh->s_full[slot]);
+        };
+        // O[slot] += P[slot] V
+        auto values = [&](int slot, int i, bool first) {
+          if (!ok) return;
+          tc_fence_after();
+          const uint32_t b = ring_addr + (i % kRing) * kTileBytes;
+#pragma unroll 1
+          for (int k = 0; k < 8; ++k)
+            umma_ts(tmem + kColO + slot * kD, tmem + kColS + slot * kTile + 8 * k,
+                    umma_desc_v(b + k * 2048), idesc_o, !(first && k == 0));
+        };
+        auto release = [&](int i) {
+          if (ok) umma_commit(&sh->empty[i % kRing]);
+        };
+        for (int u = u0; u < plan.units && plan.start(u) < x1; ++u) {
+          const Share s = share_of(plan, u, x0, x1);
+          const int T = s.t1 - s.t0;
+          if (T <= 0) continue;
+          wait(&sh->q_full, q_phase);
+          q_phase ^= 1;
+          if (s.pair) {
+            wait_tile(n);
+            scores(0, 0, n);
+            scores(1, 1, n);
+            release(n++);
+            for (int j = 0; j < T; ++j) {
+              const int v = n++;
+              const int k = j + 1 < T ? n++ : -1;
+#pragma unroll 1
+              for (int slot = 0; slot < 2; ++slot) {
+                wait(&sh->p_full[slot], (p_phases >> slot) & 1);
+                p_phases ^= 1u << slot;
+                if (slot == 0) wait_tile(v);
+                values(slot, v, j == 0);
+                if (slot == 1) release(v);
+                if (k >= 0) {
+                  if (slot == 0) wait_tile(k);
+                  scores(slot, slot, k);
+                  if (slot == 1) release(k);
+                } else if (ok) {
+                  umma_commit(&sh->o_full[slot]);
+                }
+              }
+            }
+          } else {
+            for (int j = 0; j < 2 && j < T; ++j) {
+              wait_tile(n);
+              scores(j, 0, n);
+              release(n++);
+            }
+            for (int j = 0; j < T; ++j) {
+              const int slot = j & 1;
+              const int v = n++;
+              const int k = j + 2 < T ? n++ : -1;
+              wait(&sh->p_full[slot], (p_phases >> slot) & 1);
+              p_phases ^= 1u << slot;
+              wait_tile(v);
+              values(slot, v, j < 2);
+              release(v);
+              if (k >= 0) {
+                wait_tile(k);
+                scores(slot, 0, k);
+                release(k);
+              } else if (ok) {
+                umma_commit(&sh->o_full[slot]);
+              }
+            }
+          }
+        }
+        // nothing of the tensor pipe is in flight when the memory is freed
+        umma_commit(&sh->drain);
+        if (!mbar_wait(&sh->drain, 0)) record_status(p.status, RI_ERR_TIMEOUT);
+      }
+      __syncwarp();
+    }
+  } else {
+    // ----------------------------------------------------------- softmax
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+    const int slot = warp >> 2;
+    const int row = (warp & 3) * 32 + lane;  // row of the tile = TMEM lane
+    const uint32_t lane_addr = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t t_s = tmem + lane_addr + kColS + slot * kTile;
+    const uint32_t t_o = tmem + lane_addr + kColO + slot * kD;
+    uint32_t s_phase = 0, o_phase = 0;
+    const int H = p.c.num_kv_heads, G = p.c.group_size;
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      if (ok) ok = __all_sync(~0u, mbar_wait(bar, parity));
+      if (!ok && lane == 0) record_status(p.status, RI_ERR_TIMEOUT);
+    };
+    for (int u = u0; u < plan.units && plan.start(u) < x1; ++u) {
+      const Share s = share_of(plan, u, x0, x1);
+      const int T = s.t1 - s.t0;
+      if (T <= 0) continue;
+      // the unit's query rows, into the K-major 128-byte swizzle
+      const int q_rows = s.pair ? 2 * kTile : kTile;
+      for (int i = tid; i < q_rows * 16; i += kSoftmaxWarps * 32) {
+        const int r = i >> 4, ch = i & 15;
+        const int qr = s.row0 + r;
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (qr < plan.rows)
+          v = ldg_nc_v4(p.q + (((size_t)(qr / G) * H + s.head) * G + qr % G) * kD + ch * 8);
+        uint8_t* dst = sq + (r >> 7) * kTileBytes + (ch >> 3) * kHalfTile + (r & 127) * 128 +
+                       (((ch & 7) ^ (r & 7)) << 4);
+        *reinterpret_cast<uint4*>(dst) = v;
+      }
+      fence_proxy_async_smem();
+      mbar_arrive(&sh->q_full);
+
+      const int row_tile0 = s.row0 + (s.pair ? slot * kTile : 0);
+      const bool live = row_tile0 + (warp & 3) * 32 < plan.rows;  // any row of this warp
+      const int step = s.pair ? 1 : 2;
+      float m = 0.f, l = 0.f;
+      bool any = false;
+      for (int t = s.t0 + (s.pair ? 0 : slot); t < s.t1; t += step) {
+        wait(&sh->s_full[slot], s_phase);
+        s_phase ^= 1;
+        if (ok && live) {
+          tc_fence_after();
+          uint32_t x[4][32];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_ld32_nowait(t_s + c * 32, x[c]);
+          tmem_wait_ld();
+          if (t == last_tile) {
+            const int n = p.prefix_len - t * kTile;  // valid keys, >= 1
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (c * 32 + i >= n) x[c][i] = 0xff800000u;  // -inf
+          }
+          float mx[4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            mx[c] = __uint_as_float(x[c][0]);
+#pragma unroll
+            for (int i = 1; i < 31; i += 2)
+              mx[c] = fmax3f(mx[c], __uint_as_float(x[c][i]), __uint_as_float(x[c][i + 1]));
+            mx[c] = fmaxf(mx[c], __uint_as_float(x[c][31]));
+          }
+          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * kScaleLog2;
+          if (!any) {
+            m = top;
+          } else {
+            // the numerator is complete up to the previous tile here: the
+            // commit that signalled these scores covers every MMA before it
+            const bool grow = top > m + kLazy;
+            if (__any_sync(~0u, grow)) {
+              const float mn = grow ? top : m;
+              const float f = exp2_approx(m - mn);
+              m = mn;
+              l *= f;
+              uint32_t o[16];
+#pragma unroll 1
+              for (int c = 0; c < 8; ++c) {  // 16 columns: the scores stay in registers
+                tmem_ld16(t_o + c * 16, o);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                tmem_st16(t_o + c * 16, o);
+              }
+            }
+          }
+          any = true;
+          float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+              const float a = exp2_approx(fmaf(__uint_as_float(x[c][i]), kScaleLog2, -m));
+              const float b = exp2_approx(fmaf(__uint_as_float(x[c][i + 1]), kScaleLog2, -m));
+              sum[i & 2] += a;
+              sum[(i & 2) + 1] += b;
+              pk[i >> 1] = pack_bf16(a, b);
+            }
+            tmem_st16(t_s + c * 16, pk);
+          }
+          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          tmem_wait_st();
+          tc_fence_before();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh->p_full[slot]);
+      }
+
+      // -------------------------------------------- the unit's share goes out
+      const bool used = s.pair || s.t0 + slot < s.t1;  // this slot had a tile
+      if (used) {
+        wait(&sh->o_full[slot], o_phase);
+        o_phase ^= 1;
+      }
+      const size_t out_slot = 2 * ((size_t)blockIdx.x + u) + (s.pair ? slot : 0);
+      float* num = p.pnum + out_slot * kTile * kD;
+      float* ml = p.pml + out_slot * kTile * 2;
+      const bool row_ok = row_tile0 + row < plan.rows;
+      if (s.pair) {
+        if (ok && live) {
+          tc_fence_after();
+          if (row_ok) *reinterpret_cast<float2*>(ml + row * 2) = make_float2(m, l);
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            uint32_t o[32];
+            tmem_ld32_nowait(t_o + c * 32, o);
+            tmem_wait_ld();
+            if (row_ok)
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                *reinterpret_cast<uint4*>(num + ((c * 8 + i) * kTile + row) * 4) =
+                    make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+          }
+          tc_fence_before();
+        }
+      } else {
+        // both slots hold the same rows: (m, l) change hands in the second
+        // query tile, which is free here, and each warpgroup joins half of the
+        // columns of both numerators
+        float2* ex = reinterpret_cast<float2*>(sq + kTileBytes);  // [2][128]
+        ex[slot * kTile + row] = used ? make_float2(m, l) : make_float2(-INFINITY, 0.f);
+        named_barrier(1, kSoftmaxWarps * 32);
+        const float2 e0 = ex[row], e1 = ex[kTile + row];
+        const float m0 = e0.x, l0 = e0.y, m1 = e1.x, l1 = e1.y;
+        const float M = fmaxf(m0, m1);
+        const float f0 = exp2_approx(m0 - M), f1 = exp2_approx(m1 - M);
+        const bool both = s.t1 - s.t0 > 1;
+        if (ok && live) {
+          tc_fence_after();
+          if (row_ok && slot == 0)
+            *reinterpret_cast<float2*>(ml + row * 2) = make_float2(M, f0 * l0 + f1 * l1);
+          const uint32_t t_num = tmem + lane_addr + kColO;
+#pragma unroll 1
+          for (int c = 2 * slot; c < 2 * slot + 2; ++c) {
+            uint32_t a[32], b[32];
+            tmem_ld32_nowait(t_num + c * 32, a);
+            if (both) tmem_ld32_nowait(t_num + kD + c * 32, b);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              float v = f0 * __uint_as_float(a[i]);
+              if (both) v = fmaf(f1, __uint_as_float(b[i]), v);
+              a[i] = __float_as_uint(v);
+            }
+            if (row_ok)
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                *reinterpret_cast<uint4*>(num + ((c * 8 + i) * kTile + row) * 4) =
+                    make_uint4(a[4 * i], a[4 * i + 1], a[4 * i + 2], a[4 * i + 3]);
+          }
+          tc_fence_before();
+        }
+      }
+      // the numerators are read and the query tiles done with (their last
+      // scores were waited for) before the next unit replaces either
+      named_barrier(1, kSoftmaxWarps * 32);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kWarpMma) tmem_dealloc(tmem, 512);
+}
+
+// --------------------------------------------------------------- own tokens
+// One block of four warps per (sequence, KV head, share); the share's tiles
+// of 16 tokens are dealt to the warps, each with its own ring of copies.
+constexpr int kOwnWarps = 4;
+constexpr int kOwnThreads = kOwnWarps * 32;
+constexpr int kOwnTokens = 16;
+constexpr int kOwnRing = 3;
+constexpr int kOwnTile = kOwnTokens * kD * 2;  // 4 KB of K, as much of V
+constexpr size_t kOwnSmem = (size_t)kOwnWarps * kOwnRing * 2 * kOwnTile;
+
+__device__ __forceinline__ void cp_async16_zero(uint32_t smem, const void* g, bool valid) {
+  const int n = valid ? 16 : 0;  // 0: the 16 bytes are filled with zeros, nothing is read
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem), "l"(g), "r"(n)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm_x4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm_x4_t(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
 
 __device__ __forceinline__ int live_len(const ri_token_cache& c, int unit, int* status) {
   int len = c.lens[unit];
   if (len < 0 || len > c.capacity) {
-    record_status(status, RI_ERR_INVALID_ARG);
+    if (threadIdx.x == 0) record_status(status, RI_ERR_INVALID_ARG);
     len = len < 0 ? 0 : c.capacity;
   }
   return len;
 }
 
-__global__ void __launch_bounds__(kThreads) attend_kernel(AttendParams p) {
-  __shared__ float sh_m[kWarps][kMaxGroup], sh_l[kWarps][kMaxGroup];
-  __shared__ float sh_o[kWarps][kMaxGroup][kHeadDim];
+__global__ void __launch_bounds__(kOwnThreads) own_kernel(const __grid_constant__ AttendParams p) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ float sh_m[kOwnWarps][8], sh_l[kOwnWarps][8];
   const int unit = blockIdx.x / p.splits, split = blockIdx.x % p.splits;
-  const int G = p.c.group_size, H = p.c.num_kv_heads;
-  const int b = unit / H, h = unit % H;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int G = p.c.group_size, Gp = G <= 4 ? 4 : 8;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, tq = lane & 3;  // score row (query) and column pair of a thread
+  const int cap = p.c.capacity;
   const int len = live_len(p.c, unit, p.status);
-  const int P = p.p.length;
-  const long long n = (long long)P + len;
-  const long long i0 = n * split / p.splits, i1 = n * (split + 1) / p.splits;
-  float q[kMaxGroup][4], o[kMaxGroup][4], m[kMaxGroup], l[kMaxGroup];
-  for (int g = 0; g < kMaxGroup; ++g) {
-    m[g] = -INFINITY;
-    l[g] = 0.f;
-    for (int e = 0; e < 4; ++e) {
-      o[g][e] = 0.f;
-      q[g][e] = g < G ? __bfloat162float(p.q[((size_t)b * H * G + h * G + g) * kHeadDim + lane * 4 + e])
-                      : 0.f;
+  // whole tiles of 16 tokens, split evenly
+  const int tiles = (len + kOwnTokens - 1) / kOwnTokens;
+  const int t0 = (int)((long long)tiles * split / p.splits);
+  const int t1 = (int)((long long)tiles * (split + 1) / p.splits);
+  const uint8_t* K = static_cast<const uint8_t*>(p.c.K) + (size_t)unit * cap * kD * 2;
+  const uint8_t* V = static_cast<const uint8_t*>(p.c.V) + (size_t)unit * cap * kD * 2;
+  const uint32_t buf = smem_u32(smem) + warp * kOwnRing * 2 * kOwnTile;
+
+  // chunk c (16 bytes) of row r of a tile, XOR-swizzled for ldmatrix
+  auto at = [](int r, int c) { return (uint32_t)(r * 256 + ((c ^ (r & 7)) << 4)); };
+  auto copy = [&](int t, int stage) {
+    const uint32_t dst = buf + stage * 2 * kOwnTile;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {  // two whole rows per instruction
+      const int r = 2 * i + (lane >> 4), c = lane & 15;
+      const int tok = t * kOwnTokens + r;
+      const bool valid = tok < len;
+      const size_t src = valid ? (size_t)tok * 256 + c * 16 : 0;
+      cp_async16_zero(dst + at(r, c), K + src, valid);
+      cp_async16_zero(dst + kOwnTile + at(r, c), V + src, valid);
     }
+  };
+#pragma unroll
+  for (int i = 0; i < kOwnRing - 1; ++i) {
+    if (t0 + warp + i * kOwnWarps < t1) copy(t0 + warp + i * kOwnWarps, i);
+    cp_async_commit();
   }
-  for (long long i = i0 + warp; i < i1; i += kWarps) {
-    const __nv_bfloat16 *k, *v;
-    if (i < P) {
-      k = static_cast<const __nv_bfloat16*>(p.p.K) + h * p.p.stride_h + i * p.p.stride_t;
-      v = static_cast<const __nv_bfloat16*>(p.p.V) + h * p.p.stride_h + i * p.p.stride_t;
-    } else {
-      const size_t row = (size_t)unit * p.c.capacity + (i - P);
-      k = static_cast<const __nv_bfloat16*>(p.c.K) + row * kHeadDim;
-      v = static_cast<const __nv_bfloat16*>(p.c.V) + row * kHeadDim;
+  // query rows as the A operand: rows g (valid below G), rows 8..15 are zero
+  uint32_t qa[8][2];
+  const uint32_t* q = reinterpret_cast<const uint32_t*>(
+      p.q + ((size_t)unit * G + (g < G ? g : 0)) * kD);
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    qa[k][0] = g < G ? q[k * 8 + tq] : 0u;
+    qa[k][1] = g < G ? q[k * 8 + 4 + tq] : 0u;
+  }
+  float m = -INFINITY, l = 0.f;  // of query g, over this thread's columns for l
+  float o[8][4];                 // numerator^T: rows d = 16 i + lane / 4 (+ 8), columns 2 tq, + 1
+#pragma unroll
+  for (int i = 0; i < 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+
+  int stage = 0;
+  for (int t = t0 + warp; t < t1; t += kOwnWarps) {
+    const int ahead = t + (kOwnRing - 1) * kOwnWarps;
+    if (ahead < t1) copy(ahead, (stage + kOwnRing - 1) % kOwnRing);
+    cp_async_commit();
+    cp_async_wait<kOwnRing - 1>();
+    __syncwarp();
+    const uint32_t kb = buf + stage * 2 * kOwnTile, vb = kb + kOwnTile;
+    float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      // matrices: keys 0-7 / 8-15 (lane bit 4) x the two halves of 16 d (bit 3)
+      uint32_t b[4];
+      ldsm_x4(b, kb + at((lane & 7) + ((lane >> 4) << 3), 2 * k + ((lane >> 3) & 1)));
+      mma16816(s[0], qa[k][0], 0u, qa[k][1], 0u, b[0], b[1]);
+      mma16816(s[1], qa[k][0], 0u, qa[k][1], 0u, b[2], b[3]);
     }
-    float kf[4], vf[4];
-    for (int e = 0; e < 4; ++e) {
-      kf[e] = __bfloat162float(k[lane * 4 + e]);
-      vf[e] = __bfloat162float(v[lane * 4 + e]);
+    float x[4] = {s[0][0] * kScaleLog2, s[0][1] * kScaleLog2, s[1][0] * kScaleLog2,
+                  s[1][1] * kScaleLog2};
+    const int tok = t * kOwnTokens + 2 * tq;  // tokens tok, tok + 1, tok + 8, tok + 9
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int ti = tok + (i & 1) + (i >> 1) * 8;
+      if (ti >= len) x[i] = -INFINITY;
+      else if (p.add_weight && g < G) p.score[((size_t)unit * cap + ti) * Gp + g] = x[i];
+    }
+    float top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+    top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
+    top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));  // finite: a tile has a valid token
+    const bool grow = top > m + kLazy;
+    if (__any_sync(~0u, grow)) {
+      const float mn = grow ? top : m;
+      const float f = m == -INFINITY ? 0.f : exp2_approx(m - mn);
+      m = mn;
+      l *= f;
+      const float f0 = __shfl_sync(~0u, f, 8 * tq), f1 = __shfl_sync(~0u, f, 8 * tq + 4);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        o[i][0] *= f0;
+        o[i][1] *= f1;
+        o[i][2] *= f0;
+        o[i][3] *= f1;
+      }
     }
 #pragma unroll
-    for (int g = 0; g < kMaxGroup; ++g) {
-      if (g >= G) break;
-      float s = 0.f;
-      for (int e = 0; e < 4; ++e) s += q[g][e] * kf[e];
-      for (int x = 16; x; x >>= 1) s += __shfl_xor_sync(~0u, s, x);
-      s *= kScale;
-      if (i >= P && lane == 0)
-        p.score[((size_t)unit * p.c.capacity + (i - P)) * G + g] = s;
-      const float mn = fmaxf(m[g], s);
-      const float a = __expf(m[g] - mn), w = __expf(s - mn);
-      m[g] = mn;
-      l[g] = l[g] * a + w;
-      for (int e = 0; e < 4; ++e) o[g][e] = o[g][e] * a + w * vf[e];
+    for (int i = 0; i < 4; ++i) x[i] = exp2_approx(x[i] - m);
+    l += (x[0] + x[1]) + (x[2] + x[3]);
+    const uint32_t p0 = pack_bf16(x[0], x[1]), p1 = pack_bf16(x[2], x[3]);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      // V^T: matrices keys 0-7 / 8-15 (lane bit 4) x d halves of 16 (bit 3)
+      uint32_t a[4];
+      ldsm_x4_t(a, vb + at((lane & 7) + ((lane >> 4) << 3), 2 * i + ((lane >> 3) & 1)));
+      mma16816(o[i], a[0], a[1], a[2], a[3], p0, p1);
     }
+    __syncwarp();
+    stage = (stage + 1) % kOwnRing;
   }
-  for (int g = 0; g < G; ++g) {
-    if (lane == 0) {
-      sh_m[warp][g] = m[g];
-      sh_l[warp][g] = l[g];
-    }
-    for (int e = 0; e < 4; ++e) sh_o[warp][g][lane * 4 + e] = o[g][e];
+  cp_async_wait<0>();
+  l += __shfl_xor_sync(~0u, l, 1);
+  l += __shfl_xor_sync(~0u, l, 2);
+  if (tq == 0) {
+    sh_m[warp][g] = m;
+    sh_l[warp][g] = l;
   }
+  __syncthreads();  // also: every warp is done with its ring, which now takes numerators
+  float* num = reinterpret_cast<float*>(smem);  // [warp][query][128]
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      num[(warp * 8 + 2 * tq + (e & 1)) * kD + 16 * i + g + (e >> 1) * 8] = o[i][e];
   __syncthreads();
-  for (int g = 0; g < G; ++g) {
-    float mx = -INFINITY, sum = 0.f, acc = 0.f;
-    for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, sh_m[w][g]);
-    if (mx > -INFINITY)
-      for (int w = 0; w < kWarps; ++w) {
-        const float f = __expf(sh_m[w][g] - mx);
-        sum += f * sh_l[w][g];
-        acc += f * sh_o[w][g][threadIdx.x];
+  for (int r = 0; r < G; ++r) {
+    float M = -INFINITY, sum = 0.f, acc = 0.f;
+#pragma unroll
+    for (int w = 0; w < kOwnWarps; ++w) M = fmaxf(M, sh_m[w][r]);
+    if (M > -INFINITY) {
+#pragma unroll
+      for (int w = 0; w < kOwnWarps; ++w) {
+        const float f = exp2_approx(sh_m[w][r] - M);
+        sum += f * sh_l[w][r];
+        acc += f * num[(w * 8 + r) * kD + threadIdx.x];
       }
-    const size_t at = ((size_t)unit * p.splits + split) * G + g;
-    p.num[at * kHeadDim + threadIdx.x] = acc;
-    if (threadIdx.x == 0) {
-      p.ml[at * 2] = mx;
-      p.ml[at * 2 + 1] = sum;
     }
+    const size_t i = ((size_t)unit * p.splits + split) * G + r;
+    p.num[i * kD + threadIdx.x] = acc;
+    if (threadIdx.x == 0) *reinterpret_cast<float2*>(p.ml + i * 2) = make_float2(M, sum);
   }
 }
 
-__global__ void __launch_bounds__(kThreads) merge_kernel(AttendParams p, int chunks) {
+// -------------------------------------------------------------------- merge
+// One block per (sequence, KV head) and chunk of its own tokens: every block
+// joins the references and sums of its G rows, the first one the numerators.
+constexpr int kMergeThreads = 128;
+
+__global__ void __launch_bounds__(kMergeThreads) merge_kernel(const __grid_constant__ AttendParams p, int chunks) {
   const int unit = blockIdx.x / chunks, chunk = blockIdx.x % chunks;
-  const int G = p.c.group_size, H = p.c.num_kv_heads;
+  const int G = p.c.group_size, H = p.c.num_kv_heads, Gp = G <= 4 ? 4 : 8;
   const int b = unit / H, h = unit % H;
+  const int d = threadIdx.x;
   const int len = live_len(p.c, unit, p.status);
+  const PrefixPlan& plan = p.plan;
   float lse[kMaxGroup];
 #pragma unroll
   for (int g = 0; g < kMaxGroup; ++g) {
-    if (g >= G) break;
-    float m = -INFINITY, l = 0.f;
+    lse[g] = -INFINITY;
+    if (g >= G) continue;
+    // prefix shares of row r of the head: the blocks whose work meets its unit
+    const int r = b * G + g;
+    const int u = plan.blocks ? h * plan.per_head + r / (2 * kTile) : 0;
+    const int second = r % (2 * kTile) / kTile, pr = r % kTile;
+    int c0 = 0, c1 = 0;
+    if (plan.blocks) {
+      const long long s0 = plan.start(u);
+      const long long s1 = s0 + (long long)plan.work_per_tile(u) * plan.key_tiles;
+      c0 = (int)(s0 * plan.blocks / plan.total);
+      c1 = (int)((s1 * plan.blocks + plan.total - 1) / plan.total);
+      if (c1 > plan.blocks) c1 = plan.blocks;
+    }
+    auto used = [&](int c) {
+      return plan.tile_at(u, plan.from(c)) < plan.tile_at(u, plan.from(c + 1));
+    };
+    float m = -INFINITY, l = 0.f, acc = 0.f;
+    for (int c = c0; c < c1; ++c)
+      if (used(c)) m = fmaxf(m, p.pml[((2 * ((size_t)c + u) + second) * kTile + pr) * 2]);
     for (int s = 0; s < p.splits; ++s)
       m = fmaxf(m, p.ml[(((size_t)unit * p.splits + s) * G + g) * 2]);
-    if (m > -INFINITY)
-      for (int s = 0; s < p.splits; ++s) {
-        const float* ml = p.ml + (((size_t)unit * p.splits + s) * G + g) * 2;
-        l += __expf(ml[0] - m) * ml[1];
+    if (m > -INFINITY) {
+      for (int c = c0; c < c1; ++c) {
+        if (!used(c)) continue;
+        const size_t slot = 2 * ((size_t)c + u) + second;
+        const float2 v = *reinterpret_cast<const float2*>(p.pml + (slot * kTile + pr) * 2);
+        const float f = exp2_approx(v.x - m);
+        l += f * v.y;
+        if (chunk == 0)
+          acc += f * p.pnum[slot * kTile * kD + ((d >> 2) * kTile + pr) * 4 + (d & 3)];
       }
-    lse[g] = l > 0.f ? m + logf(l) : -INFINITY;
+      for (int s = 0; s < p.splits; ++s) {
+        const size_t i = ((size_t)unit * p.splits + s) * G + g;
+        const float2 v = *reinterpret_cast<const float2*>(p.ml + i * 2);
+        const float f = exp2_approx(v.x - m);
+        l += f * v.y;
+        if (chunk == 0) acc += f * p.num[i * kD + d];
+      }
+      lse[g] = m + log2f(l);
+    }
     if (chunk == 0) {
-      float acc = 0.f;
-      if (l > 0.f)
-        for (int s = 0; s < p.splits; ++s) {
-          const size_t at = ((size_t)unit * p.splits + s) * G + g;
-          acc += __expf(p.ml[at * 2] - m) * p.num[at * kHeadDim + threadIdx.x];
-        }
-      const size_t row = (size_t)b * H * G + h * G + g;
-      p.out[row * kHeadDim + threadIdx.x] = __float2bfloat16_rn(l > 0.f ? acc / l : 0.f);
-      if (p.lse && threadIdx.x == 0) p.lse[row] = lse[g];
+      const size_t row = (size_t)unit * G + g;
+      p.out[row * kD + d] = __float2bfloat16_rn(l > 0.f ? acc / l : 0.f);
+      if (p.lse && d == 0) p.lse[row] = lse[g] * kLn2;
     }
   }
   if (!p.add_weight) return;
-  for (int i = chunk * kThreads + threadIdx.x; i < len; i += chunks * kThreads) {
+  for (int i = chunk * kMergeThreads + d; i < len; i += chunks * kMergeThreads) {
     const size_t row = (size_t)unit * p.c.capacity + i;
+    const float4* s = reinterpret_cast<const float4*>(p.score + row * Gp);
     float w = 0.f;
-#pragma unroll
-    for (int g = 0; g < kMaxGroup; ++g)
-      if (g < G) w += __expf(p.score[row * G + g] - lse[g]);
+    const float4 a = s[0];
+    w += exp2_approx(a.x - lse[0]);
+    if (G > 1) w += exp2_approx(a.y - lse[1]);
+    if (G > 2) w += exp2_approx(a.z - lse[2]);
+    if (G > 3) w += exp2_approx(a.w - lse[3]);
+    if (G > 4) {
+      const float4 e = s[1];
+      w += exp2_approx(e.x - lse[4]);
+      if (G > 5) w += exp2_approx(e.y - lse[5]);
+      if (G > 6) w += exp2_approx(e.z - lse[6]);
+      if (G > 7) w += exp2_approx(e.w - lse[7]);
+    }
     p.c.weight[row] += w;
   }
+}
+
+// --------------------------------------------------------------------- host
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_fn() {
+  static const EncodeTiledFn fn = [] {
+    void* ptr = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault, &q) ==
+            cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      return reinterpret_cast<EncodeTiledFn>(ptr);
+    return static_cast<EncodeTiledFn>(nullptr);
+  }();
+  return fn;
+}
+
+// [heads][length][128] bf16 with the prefix's strides, boxes of 128 tokens x
+// 64 columns (128-byte swizzle); rows past the length read as zero.
+cudaError_t encode_prefix(CUtensorMap* map, const void* base, const ri_token_prefix& p,
+                          int heads) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return cudaErrorNotSupported;
+  cuuint64_t dims[3] = {(cuuint64_t)kD, (cuuint64_t)p.length, (cuuint64_t)heads};
+  cuuint64_t strides[2] = {(cuuint64_t)p.stride_t * 2, (cuuint64_t)p.stride_h * 2};
+  cuuint32_t box[3] = {64, kTile, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box,
+            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+             ? cudaSuccess
+             : cudaErrorInvalidValue;
 }
 
 }  // namespace
 
 size_t token_attend_bytes(const ri_token_cache& c, int prefix_len) {
-  return layout(c, prefix_len).total;
+  return layout(c, plan_prefix(c, prefix_len)).total;
 }
 
 cudaError_t launch_token_attend(const TokenAttendArgs& a, cudaStream_t s) {
-  const AttendLayout L = layout(a.c, a.p.length);
   AttendParams p;
+  memset(&p, 0, sizeof(p));
+  p.plan = plan_prefix(a.c, a.p.length);
+  const AttendLayout L = layout(a.c, p.plan);
   p.c = a.c;
-  p.p = a.p;
   p.q = static_cast<const __nv_bfloat16*>(a.q);
   p.out = static_cast<__nv_bfloat16*>(a.out);
   p.lse = a.lse;
+  p.pml = reinterpret_cast<float*>(a.ws + L.off_pml);
+  p.pnum = reinterpret_cast<float*>(a.ws + L.off_pnum);
   p.ml = reinterpret_cast<float*>(a.ws + L.off_ml);
   p.num = reinterpret_cast<float*>(a.ws + L.off_num);
   p.score = reinterpret_cast<float*>(a.ws + L.off_score);
   p.status = reinterpret_cast<int*>(a.ws);
+  p.prefix_len = a.p.length;
   p.splits = L.splits;
   p.add_weight = a.add_weight;
-  const int units = a.c.batch * a.c.num_kv_heads;
-  attend_kernel<<<units * L.splits, kThreads, 0, s>>>(p);
-  cudaError_t e = cudaGetLastError();
+  cudaError_t e = set_smem_once(5, reinterpret_cast<const void*>(own_kernel), (int)kOwnSmem);
   if (e != cudaSuccess) return e;
-  int chunks = a.add_weight ? (a.c.capacity + kThreads * 4 - 1) / (kThreads * 4) : 1;
-  merge_kernel<<<units * chunks, kThreads, 0, s>>>(p, chunks);
+  if (p.plan.blocks) {
+    CUtensorMap mk, mv;
+    e = set_smem_once(4, reinterpret_cast<const void*>(prefix_kernel), (int)kPrefixSmem);
+    if (e == cudaSuccess) e = encode_prefix(&mk, a.p.K, a.p, a.c.num_kv_heads);
+    if (e == cudaSuccess) e = encode_prefix(&mv, a.p.V, a.p, a.c.num_kv_heads);
+    if (e != cudaSuccess) return e;
+    prefix_kernel<<<p.plan.blocks, kPrefixThreads, kPrefixSmem, s>>>(mk, mv, p);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  }
+  const int units = a.c.batch * a.c.num_kv_heads;
+  own_kernel<<<units * L.splits, kOwnThreads, kOwnSmem, s>>>(p);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  const int chunks =
+      a.add_weight ? (a.c.capacity + 4 * kMergeThreads - 1) / (4 * kMergeThreads) : 1;
+  merge_kernel<<<units * chunks, kMergeThreads, 0, s>>>(p, chunks);
   return cudaGetLastError();
 }
 
