@@ -258,6 +258,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const PrefixPlan& plan = p.plan;
 
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (warp == kWarpMma) {
     tmem_alloc(&sh->tmem, 512);
     tmem_relinquish();
@@ -660,6 +661,7 @@ __device__ __forceinline__ int live_len(const ri_token_cache& c, int unit, int* 
 __global__ void __launch_bounds__(kOwnThreads) own_kernel(const __grid_constant__ AttendParams p) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float sh_m[kOwnWarps][8], sh_l[kOwnWarps][8];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int unit = blockIdx.x / p.splits, split = blockIdx.x % p.splits;
   const int G = p.c.group_size, Gp = G <= 4 ? 4 : 8;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -796,72 +798,120 @@ __global__ void __launch_bounds__(kOwnThreads) own_kernel(const __grid_constant_
     p.num[i * kD + threadIdx.x] = acc;
     if (threadIdx.x == 0) *reinterpret_cast<float2*>(p.ml + i * 2) = make_float2(M, sum);
   }
+  // this launch completes after the prefix launch, so that the merge, which
+  // waits for this one, has both
+  asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // -------------------------------------------------------------------- merge
-// One block per (sequence, KV head) and chunk of its own tokens: every block
-// joins the references and sums of its G rows, the first one the numerators.
-constexpr int kMergeThreads = 128;
+// One block per (sequence, KV head) and chunk of its own tokens.  Every block
+// joins the references and sums of its G rows (a warp per row, its lanes over
+// the shares); the first one also joins the numerators, four rows at a time,
+// with the shares' factors in shared memory.
+constexpr int kMergeThreads = 512;
 
-__global__ void __launch_bounds__(kMergeThreads) merge_kernel(const __grid_constant__ AttendParams p, int chunks) {
+__global__ void __launch_bounds__(kMergeThreads)
+    merge_kernel(const __grid_constant__ AttendParams p, int chunks) {
+  extern __shared__ float factor[];  // [G][shares]: reference, then 2^(m - M)
+  __shared__ float sh_lse[kMaxGroup], sh_l[kMaxGroup];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int unit = blockIdx.x / chunks, chunk = blockIdx.x % chunks;
   const int G = p.c.group_size, H = p.c.num_kv_heads, Gp = G <= 4 ? 4 : 8;
   const int b = unit / H, h = unit % H;
-  const int d = threadIdx.x;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int len = live_len(p.c, unit, p.status);
   const PrefixPlan& plan = p.plan;
-  float lse[kMaxGroup];
+  const int shares = plan.blocks + p.splits;  // room per row; most rows use fewer
+  // A row's prefix shares come from blocks c0 .. c1 - 1 (the G rows of a
+  // sequence may lie in two row tiles, even in two units).
+  auto unit_of_row = [&](int r) { return h * plan.per_head + r / (2 * kTile); };
+  auto block_range = [&](int u, int* c0, int* c1) {
+    *c0 = *c1 = 0;
+    if (!plan.blocks) return;
+    const long long s0 = plan.start(u);
+    const long long s1 = s0 + (long long)plan.work_per_tile(u) * plan.key_tiles;
+    *c0 = (int)(s0 * plan.blocks / plan.total);
+    const int e = (int)((s1 * plan.blocks + plan.total - 1) / plan.total);
+    *c1 = e < plan.blocks ? e : plan.blocks;
+  };
+  if (warp < G) {
+    const int g = warp, r = b * G + g;
+    const int u = plan.blocks ? unit_of_row(r) : 0;
+    int c0, c1;
+    block_range(u, &c0, &c1);
+    const int second = r / kTile & 1, pr = r % kTile;
+    const int n_prefix = c1 - c0;
+    float* f = factor + (size_t)g * shares;
+    float m = -INFINITY, l = 0.f;
+    for (int i = lane; i < n_prefix + p.splits; i += 32) {
+      float2 v = make_float2(-INFINITY, 0.f);
+      if (i < n_prefix) {
+        const int c = c0 + i;
+        // (a block on the unit's edge may have no tile of it)
+        if (plan.tile_at(u, plan.from(c)) < plan.tile_at(u, plan.from(c + 1)))
+          v = *reinterpret_cast<const float2*>(
+              p.pml + ((2 * ((size_t)c + u) + second) * kTile + pr) * 2);
+      } else {
+        v = *reinterpret_cast<const float2*>(
+            p.ml + (((size_t)unit * p.splits + i - n_prefix) * G + g) * 2);
+      }
+      f[i] = v.x;
+      if (v.x > m) {
+        l = l * exp2_approx(m - v.x) + v.y;
+        m = v.x;
+      } else if (v.x > -INFINITY) {
+        l += v.y * exp2_approx(v.x - m);
+      }
+    }
+    float M = m;
 #pragma unroll
-  for (int g = 0; g < kMaxGroup; ++g) {
-    lse[g] = -INFINITY;
-    if (g >= G) continue;
-    // prefix shares of row r of the head: the blocks whose work meets its unit
-    const int r = b * G + g;
-    const int u = plan.blocks ? h * plan.per_head + r / (2 * kTile) : 0;
-    const int second = r % (2 * kTile) / kTile, pr = r % kTile;
-    int c0 = 0, c1 = 0;
-    if (plan.blocks) {
-      const long long s0 = plan.start(u);
-      const long long s1 = s0 + (long long)plan.work_per_tile(u) * plan.key_tiles;
-      c0 = (int)(s0 * plan.blocks / plan.total);
-      c1 = (int)((s1 * plan.blocks + plan.total - 1) / plan.total);
-      if (c1 > plan.blocks) c1 = plan.blocks;
+    for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(~0u, M, o));
+    l = m > -INFINITY ? l * exp2_approx(m - M) : 0.f;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(~0u, l, o);
+    for (int i = lane; i < n_prefix + p.splits; i += 32)
+      f[i] = f[i] > -INFINITY ? exp2_approx(f[i] - M) : 0.f;
+    if (lane == 0) {
+      sh_l[g] = l;
+      sh_lse[g] = l > 0.f ? M + log2f(l) : -INFINITY;
     }
-    auto used = [&](int c) {
-      return plan.tile_at(u, plan.from(c)) < plan.tile_at(u, plan.from(c + 1));
-    };
-    float m = -INFINITY, l = 0.f, acc = 0.f;
-    for (int c = c0; c < c1; ++c)
-      if (used(c)) m = fmaxf(m, p.pml[((2 * ((size_t)c + u) + second) * kTile + pr) * 2]);
-    for (int s = 0; s < p.splits; ++s)
-      m = fmaxf(m, p.ml[(((size_t)unit * p.splits + s) * G + g) * 2]);
-    if (m > -INFINITY) {
-      for (int c = c0; c < c1; ++c) {
-        if (!used(c)) continue;
-        const size_t slot = 2 * ((size_t)c + u) + second;
-        const float2 v = *reinterpret_cast<const float2*>(p.pml + (slot * kTile + pr) * 2);
-        const float f = exp2_approx(v.x - m);
-        l += f * v.y;
-        if (chunk == 0)
-          acc += f * p.pnum[slot * kTile * kD + ((d >> 2) * kTile + pr) * 4 + (d & 3)];
+  }
+  __syncthreads();
+  if (chunk == 0) {
+    const int d = threadIdx.x & 127;
+    for (int g = threadIdx.x >> 7; g < G; g += kMergeThreads / 128) {
+      const int r = b * G + g;
+      const int u = plan.blocks ? unit_of_row(r) : 0;
+      int c0, c1;
+      block_range(u, &c0, &c1);
+      const float* f = factor + (size_t)g * shares;
+      const float* src = p.pnum + 2 * ((size_t)c0 + u) * kTile * kD +
+                         (size_t)(r / kTile & 1) * kTile * kD +
+                         ((d >> 2) * kTile + r % kTile) * 4 + (d & 3);
+      const int n = c1 - c0;
+      float acc = 0.f;
+#pragma unroll 8
+      for (int i = 0; i < n; ++i) {
+        const float w = f[i];  // 0: the share was not written
+        if (w > 0.f) acc = fmaf(w, src[(size_t)i * 2 * kTile * kD], acc);
       }
-      for (int s = 0; s < p.splits; ++s) {
-        const size_t i = ((size_t)unit * p.splits + s) * G + g;
-        const float2 v = *reinterpret_cast<const float2*>(p.ml + i * 2);
-        const float f = exp2_approx(v.x - m);
-        l += f * v.y;
-        if (chunk == 0) acc += f * p.num[i * kD + d];
+      const float* own = p.num + ((size_t)unit * p.splits * G + g) * kD + d;
+#pragma unroll 4
+      for (int i = 0; i < p.splits; ++i) {
+        const float w = f[n + i];
+        acc = fmaf(w, own[(size_t)i * G * kD], acc);
       }
-      lse[g] = m + log2f(l);
-    }
-    if (chunk == 0) {
+      const float l = sh_l[g];
       const size_t row = (size_t)unit * G + g;
       p.out[row * kD + d] = __float2bfloat16_rn(l > 0.f ? acc / l : 0.f);
-      if (p.lse && d == 0) p.lse[row] = lse[g] * kLn2;
+      if (p.lse && d == 0) p.lse[row] = sh_lse[g] * kLn2;
     }
   }
   if (!p.add_weight) return;
-  for (int i = chunk * kMergeThreads + d; i < len; i += chunks * kMergeThreads) {
+  float lse[kMaxGroup];
+#pragma unroll
+  for (int g = 0; g < kMaxGroup; ++g) lse[g] = g < G ? sh_lse[g] : 0.f;
+  for (int i = chunk * kMergeThreads + threadIdx.x; i < len; i += chunks * kMergeThreads) {
     const size_t row = (size_t)unit * p.c.capacity + i;
     const float4* s = reinterpret_cast<const float4*>(p.score + row * Gp);
     float w = 0.f;
@@ -918,6 +968,22 @@ cudaError_t encode_prefix(CUtensorMap* map, const void* base, const ri_token_pre
              : cudaErrorInvalidValue;
 }
 
+template <typename... Args, typename... Given>
+cudaError_t launch_dependent(void (*kernel)(Args...), int blocks, int threads, size_t smem,
+                             cudaStream_t s, bool dependent, const Given&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)blocks);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = dependent ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 }  // namespace
 
 size_t token_attend_bytes(const ri_token_cache& c, int prefix_len) {
@@ -954,12 +1020,15 @@ cudaError_t launch_token_attend(const TokenAttendArgs& a, cudaStream_t s) {
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
   const int units = a.c.batch * a.c.num_kv_heads;
-  own_kernel<<<units * L.splits, kOwnThreads, kOwnSmem, s>>>(p);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  const int chunks =
-      a.add_weight ? (a.c.capacity + 4 * kMergeThreads - 1) / (4 * kMergeThreads) : 1;
-  merge_kernel<<<units * chunks, kMergeThreads, 0, s>>>(p, chunks);
-  return cudaGetLastError();
+  // The prefix launch is ordered like any other; the two after it may start
+  // while it runs (programmatic dependent launch): the own tokens' blocks
+  // share nothing with it and fill the SMs it leaves, the merge waits for both.
+  e = launch_dependent(own_kernel, units * L.splits, kOwnThreads, kOwnSmem, s, p.plan.blocks > 0,
+                       p);
+  if (e != cudaSuccess) return e;
+  const int chunks = a.add_weight ? (a.c.capacity + 2 * kMergeThreads - 1) / (2 * kMergeThreads) : 1;
+  const size_t smem = (size_t)a.c.group_size * (p.plan.blocks + L.splits) * sizeof(float);
+  return launch_dependent(merge_kernel, units * chunks, kMergeThreads, smem, s, true, p, chunks);
 }
 
 }  // namespace ri
