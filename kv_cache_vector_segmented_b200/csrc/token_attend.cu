@@ -146,6 +146,14 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return r;
 }
 
+// True in one lane of a converged warp, the same one each time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n"
+               : "=r"(p));
+  return p != 0;
+}
+
 __device__ __forceinline__ void named_barrier(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
@@ -255,7 +263,8 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
   uint8_t* sq = base;                       // 2 query tiles
   uint8_t* ring = base + 2 * kTileBytes;    // kRing K / V tiles
   PrefixShared* sh = reinterpret_cast<PrefixShared*>(ring + kRing * kTileBytes);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // (shuffled: uniform over the warp for the compiler too)
+  const int tid = threadIdx.x, warp = __shfl_sync(~0u, tid >> 5, 0), lane = tid & 31;
   const PrefixPlan& plan = p.plan;
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -280,7 +289,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = sh->tmem;
+  const uint32_t tmem = __shfl_sync(~0u, sh->tmem, 0);
 
   const long long x0 = plan.from(blockIdx.x), x1 = plan.from(blockIdx.x + 1);
   const int u0 = plan.unit_of(x0);
@@ -328,46 +337,57 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
       __syncwarp();
     } else if (warp == kWarpMma) {
       // -------------------------------------------------------- MMA issuer
-      if (lane == 0) {
+      // The whole warp runs the loop and one elected lane issues: with the
+      // control flow and the addresses uniform over the warp an MMA takes a
+      // few issue slots (from a lane-0 branch: about 130 cycles each, more
+      // than the MMA itself).
+      {
         constexpr uint32_t idesc_s = umma_idesc_bf16_f32(kTile, kTile);
         constexpr uint32_t idesc_o = umma_idesc_bf16_f32(kTile, kD) | (1u << 16);  // B: MN major
         const uint32_t q_addr = smem_u32(sq), ring_addr = smem_u32(ring);
         int n = 0;  // tiles consumed
         uint32_t q_phase = 0, p_phases = 0;  // bit i of p_phases: slot i
         auto wait = [&](uint64_t* bar, uint32_t parity) {
-          if (ok && !mbar_wait(bar, parity)) {
-            record_status(p.status, RI_ERR_TIMEOUT);
-            ok = false;
+          if (ok) {
+            ok = __all_sync(~0u, mbar_wait(bar, parity));
+            if (!ok && lane == 0) record_status(p.status, RI_ERR_TIMEOUT);
           }
         };
         auto wait_tile = [&](int i) { wait(&sh->full[i % kRing], (uint32_t)((i / kRing) & 1)); };
+        auto commit = [&](uint64_t* bar) {
+          if (ok && elect_one()) umma_commit(bar);
+        };
         // S[slot] = Q K^T for the tile in ring slot i % kRing
         auto scores = [&](int slot, int qtile, int i) {
           if (!ok) return;
           tc_fence_after();
-          const uint32_t a = q_addr + qtile * kTileBytes;
-          const uint32_t b = ring_addr + (i % kRing) * kTileBytes;
-#pragma unroll 1
-          for (int k = 0; k < 8; ++k) {  // rolled: one thread issues, registers are short here
-            const uint32_t off = (k >> 2) * kHalfTile + (k & 3) * 32;
-            umma_bf16(tmem + kColS + slot * kTile, umma_desc_sw128(a + off),
-                      umma_desc_sw128(b + off), idesc_s, k > 0);
+          const uint64_t a = umma_desc_sw128(q_addr + qtile * kTileBytes);
+          const uint64_t b = umma_desc_sw128(ring_addr + (i % kRing) * kTileBytes);
+          const uint32_t d = tmem + kColS + slot * kTile;
+          if (elect_one()) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const uint32_t off = ((k >> 2) * kHalfTile + (k & 3) * 32) >> 4;
+              umma_bf16(d, a + off, b + off, idesc_s, k > 0);
+            }
+            umma_commit(&sh->s_full[slot]);
           }
-          umma_commit(&sh->s_full[slot]);
+          __syncwarp();
         };
         // O[slot] += P[slot] V
         auto values = [&](int slot, int i, bool first) {
           if (!ok) return;
           tc_fence_after();
-          const uint32_t b = ring_addr + (i % kRing) * kTileBytes;
-#pragma unroll 1
-          for (int k = 0; k < 8; ++k)
-            umma_ts(tmem + kColO + slot * kD, tmem + kColS + slot * kTile + 8 * k,
-                    umma_desc_v(b + k * 2048), idesc_o, !(first && k == 0));
+          const uint64_t b = umma_desc_v(ring_addr + (i % kRing) * kTileBytes);
+          const uint32_t d = tmem + kColO + slot * kD, a = tmem + kColS + slot * kTile;
+          if (elect_one()) {
+            umma_ts(d, a, b, idesc_o, !first);
+#pragma unroll
+            for (int k = 1; k < 8; ++k) umma_ts(d, a + 8 * k, b + k * (2048 >> 4), idesc_o, 1);
+          }
+          __syncwarp();
         };
-        auto release = [&](int i) {
-          if (ok) umma_commit(&sh->empty[i % kRing]);
-        };
+        auto release = [&](int i) { commit(&sh->empty[i % kRing]); };
         for (int u = u0; u < plan.units && plan.start(u) < x1; ++u) {
           const Share s = share_of(plan, u, x0, x1);
           const int T = s.t1 - s.t0;
@@ -393,8 +413,8 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
                   if (slot == 0) wait_tile(k);
                   scores(slot, slot, k);
                   if (slot == 1) release(k);
-                } else if (ok) {
-                  umma_commit(&sh->o_full[slot]);
+                } else {
+                  commit(&sh->o_full[slot]);
                 }
               }
             }
@@ -417,14 +437,14 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
                 wait_tile(k);
                 scores(slot, 0, k);
                 release(k);
-              } else if (ok) {
-                umma_commit(&sh->o_full[slot]);
+              } else {
+                commit(&sh->o_full[slot]);
               }
             }
           }
         }
         // nothing of the tensor pipe is in flight when the memory is freed
-        umma_commit(&sh->drain);
+        if (elect_one()) umma_commit(&sh->drain);
         if (!mbar_wait(&sh->drain, 0)) record_status(p.status, RI_ERR_TIMEOUT);
       }
       __syncwarp();
@@ -447,17 +467,25 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
       const Share s = share_of(plan, u, x0, x1);
       const int T = s.t1 - s.t0;
       if (T <= 0) continue;
-      // the unit's query rows, into the K-major 128-byte swizzle
-      const int q_rows = s.pair ? 2 * kTile : kTile;
-      for (int i = tid; i < q_rows * 16; i += kSoftmaxWarps * 32) {
-        const int r = i >> 4, ch = i & 15;
-        const int qr = s.row0 + r;
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (qr < plan.rows)
-          v = ldg_nc_v4(p.q + (((size_t)(qr / G) * H + s.head) * G + qr % G) * kD + ch * 8);
-        uint8_t* dst = sq + (r >> 7) * kTileBytes + (ch >> 3) * kHalfTile + (r & 127) * 128 +
-                       (((ch & 7) ^ (r & 7)) << 4);
-        *reinterpret_cast<uint4*>(dst) = v;
+      // the unit's query rows, into the K-major 128-byte swizzle: a thread
+      // takes chunk tid % 16 of every 16th row, eight loads in flight
+      for (int tile = 0; tile < (s.pair ? 2 : 1); ++tile) {
+        uint4 v[8];
+        const int ch = tid & 15;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int qr = s.row0 + tile * kTile + i * 16 + (tid >> 4);
+          const int qb = qr / G;
+          v[i] = make_uint4(0, 0, 0, 0);
+          if (qr < plan.rows)
+            v[i] = ldg_nc_v4(p.q + (((size_t)qb * H + s.head) * G + (qr - qb * G)) * kD + ch * 8);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int r = i * 16 + (tid >> 4);
+          *reinterpret_cast<uint4*>(sq + tile * kTileBytes + (ch >> 3) * kHalfTile + r * 128 +
+                                    (((ch & 7) ^ (r & 7)) << 4)) = v[i];
+        }
       }
       fence_proxy_async_smem();
       mbar_arrive(&sh->q_full);
