@@ -213,7 +213,9 @@ size_t ri_token_attend_workspace(const ri_token_cache* cache, int32_t prefix_len
     set_error("prefix length must be in [0, 2^28] (got %d)", prefix_len);
     return 0;
   }
-  return token_attend_bytes(*cache, prefix_len);
+  const size_t n = token_attend_bytes(*cache, prefix_len);
+  if (n == 0) set_error("prefix of %d tokens: too much work for one call", prefix_len);
+  return n;
 }
 
 ri_status ri_token_attend(const ri_token_cache* cache, const void* q,
@@ -241,6 +243,8 @@ ri_status ri_token_attend(const ri_token_cache* cache, const void* q,
     if (cache->num_kv_heads == 1) a.p.stride_h = a.p.stride_t;
   }
   const size_t need = token_attend_bytes(*cache, a.p.length);
+  RI_CHECK(need, RI_ERR_UNSUPPORTED, "prefix of %d tokens: too much work for one call",
+           a.p.length);
   if ((st = check_workspace(workspace, workspace_bytes, need)) != RI_OK) return st;
   a.c = *cache;
   a.q = q;

@@ -28,6 +28,7 @@ namespace {
 constexpr float kScaleLog2 = 0.08838834764831845f * 1.4426950408889634f;  // log2(e) / sqrt(128)
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kD = kHeadDim;
+constexpr float kLazy = 8.f;  // log2: the reference moves when the maximum passes it by this
 constexpr int kTile = 128;                  // query rows, keys of a tile
 constexpr int kTileBytes = kTile * kD * 2;  // 32 KB of bf16
 constexpr int kHalfTile = kTileBytes / 2;   // 64 of the 128 columns, 128-byte rows
@@ -37,58 +38,64 @@ constexpr int kHalfTile = kTileBytes / 2;   // 64 of the 128 columns, 128-byte r
 // (b, g in order) into tiles of 128.  A unit is a KV head and two row tiles
 // that share each key tile from shared memory (the last unit of an odd count
 // has one); its work is 2 (or 1) per key tile.  Block c takes the work from
-// total * c / blocks to total * (c + 1) / blocks of all units in a row, so
-// every block carries the same share to within a tile, whatever the lengths.
-// Block c's share of unit u lies in slots 2 (c + u) and 2 (c + u) + 1, which
-// no other (c, u) has, as u grows with c.
+// chunk * c to chunk * (c + 1) of all units in a row, so every block carries
+// the same share to within a tile, whatever the lengths.  Block c's share of
+// unit u lies in slots 2 (c + u) and 2 (c + u) + 1, which no other (c, u)
+// has, as u grows with c.
 struct PrefixPlan {
   int rows;            // B * G, rows per KV head
   int tiles;           // row tiles per KV head
   int per_head;        // units per KV head
   int units;           // over all KV heads
   int key_tiles;
-  int blocks;
-  long long head_work, total;  // work per KV head, in all
+  int blocks, chunk;   // chunk: work of a block
+  int head_work, total;  // work per KV head, in all
   __host__ __device__ int work_per_tile(int u) const {
     return (u % per_head) * 2 + 1 < tiles ? 2 : 1;
   }
-  __host__ __device__ long long start(int u) const {
-    return (u / per_head) * head_work + (long long)(u % per_head) * 2 * key_tiles;
+  __host__ __device__ int start(int u) const {
+    return (u / per_head) * head_work + (u % per_head) * 2 * key_tiles;
   }
-  __host__ __device__ int tile_at(int u, long long x) const {  // first key tile at or past x
-    const long long s = x - start(u);
+  __host__ __device__ int tile_at(int u, int x) const {  // first key tile at or past work x
+    const int s = x - start(u);
     if (s <= 0) return 0;
     const int w = work_per_tile(u);
-    const long long t = (s + w - 1) >> (w - 1);
-    return t < key_tiles ? (int)t : key_tiles;
+    const int t = (s >> (w - 1)) + (s & (w - 1));
+    return t < key_tiles ? t : key_tiles;
   }
-  __host__ __device__ long long from(int c) const { return total * c / blocks; }
-  __host__ __device__ int unit_of(long long x) const {  // the unit holding work x
-    const int h = (int)(x / head_work);
-    const int i = (int)((x - h * head_work) / (2ll * key_tiles));
+  __host__ __device__ int from(int c) const { return c < blocks ? c * chunk : total; }
+  __host__ __device__ int unit_of(int x) const {  // the unit holding work x
+    const int h = x / head_work;
+    const int i = (x - h * head_work) / (2 * key_tiles);
     return h * per_head + (i < per_head ? i : per_head - 1);
   }
 };
 
-PrefixPlan plan_prefix(const ri_token_cache& c, int prefix_len) {
-  PrefixPlan p = {};
-  p.rows = c.batch * c.group_size;
-  p.tiles = (p.rows + kTile - 1) / kTile;
-  p.per_head = (p.tiles + 1) / 2;
-  p.units = c.num_kv_heads * p.per_head;
-  p.key_tiles = (prefix_len + kTile - 1) / kTile;
-  p.head_work = (long long)p.tiles * p.key_tiles;
-  p.total = p.head_work * c.num_kv_heads;
-  const long long pieces = (long long)p.units * p.key_tiles;
-  const int sms = num_sms();
-  p.blocks = (int)(pieces < sms ? pieces : sms);
-  return p;
+// False when the work of all units does not fit 31 bits.
+bool plan_prefix(const ri_token_cache& c, int prefix_len, PrefixPlan* p) {
+  *p = PrefixPlan{};
+  p->rows = c.batch * c.group_size;
+  p->tiles = (p->rows + kTile - 1) / kTile;
+  p->per_head = (p->tiles + 1) / 2;
+  p->units = c.num_kv_heads * p->per_head;
+  p->key_tiles = (prefix_len + kTile - 1) / kTile;
+  const long long total = (long long)p->tiles * p->key_tiles * c.num_kv_heads;
+  if (total > (1ll << 31) - (1 << 24)) return false;
+  p->head_work = p->tiles * p->key_tiles;
+  p->total = (int)total;
+  if (!prefix_len) return true;
+  const long long pieces = (long long)p->units * p->key_tiles;
+  const int blocks = (int)(pieces < num_sms() ? pieces : num_sms());
+  p->chunk = (p->total + blocks - 1) / blocks;
+  p->blocks = (p->total + p->chunk - 1) / p->chunk;
+  return true;
 }
 
+constexpr int kMaxSplits = 512;  // bounds the merge's shared memory (8 x (SMs + 512) floats)
+
 struct AttendLayout {
-  int splits;  // shares of a (sequence, KV head)'s own tokens
-  // prefix shares: ml fp32 [slots][128][2], num fp32 [slots][32][128][4] (four
-  // columns of every row, so that a warp's rows store 512 contiguous bytes);
+  int splits;  // shares of a (sequence, KV head)'s own tokens, a warp's work each
+  // prefix shares: ml fp32 [slots][128][2], num fp32 [slots][128 rows][128];
   // own shares: ml [units][splits][G][2], num [units][splits][G][128];
   // score fp32 [units][capacity][Gp], Gp = 4 or 8
   size_t off_pml, off_pnum, off_ml, off_num, off_score, total;
@@ -97,10 +104,12 @@ struct AttendLayout {
 AttendLayout layout(const ri_token_cache& c, const PrefixPlan& pp) {
   AttendLayout L;
   const size_t units = (size_t)c.batch * c.num_kv_heads;
-  // own shares: four blocks per SM in all, none of fewer than 64 tokens
-  long long splits = (4 * 148 + units - 1) / units;
+  // own shares: about 16 per SM in all (two rounds of 8 warps), of 64 tokens
+  // or more of a full cache
+  long long splits = (16 * num_sms() + (long long)units - 1) / (long long)units;
   const long long most = (c.capacity + 63) / 64;
   if (splits > most) splits = most;
+  if (splits > kMaxSplits) splits = kMaxSplits;
   L.splits = (int)splits;
   const size_t slots = pp.blocks ? 2 * (size_t)(pp.blocks + pp.units) : 0;
   size_t off = kStatusBytesHost;
@@ -118,6 +127,8 @@ AttendLayout layout(const ri_token_cache& c, const PrefixPlan& pp) {
   return L;
 }
 
+constexpr size_t kTaskCounter = 128;  // byte of the status region: own tasks taken
+
 struct AttendParams {
   ri_token_cache c;
   const __nv_bfloat16* q;
@@ -131,6 +142,8 @@ struct AttendParams {
   int* status;
   PrefixPlan plan;  // blocks == 0: no prefix
   int prefix_len;
+  int* next_task;  // own tasks taken, in the workspace's status region; 0 between calls
+  int tasks;       // own tasks: units * splits
   int splits, add_weight;
 };
 
@@ -158,26 +171,231 @@ __device__ __forceinline__ void named_barrier(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
+// --------------------------------------------------------------- own tokens
+// A warp's task: one share of a (sequence, KV head)'s own tokens, in tiles of
+// 16 tokens through a ring of asynchronous copies.  S = Q K^T on m16n8k16
+// tiles (the G <= 8 query rows of 16), whose fragment is, as it stands, the
+// B operand of num^T += V^T P^T.
+constexpr int kOwnWarps = 4;
+constexpr int kOwnThreads = kOwnWarps * 32;
+constexpr int kOwnTokens = 16;
+constexpr int kOwnTile = kOwnTokens * kD * 2;  // 4 KB of K, as much of V
+constexpr int kOwnStages = 3;        // of a block of its own
+constexpr int kOwnStagesBeside = 2;  // of a warp beside the prefix
+constexpr size_t own_ring_bytes(int stages) { return (size_t)stages * 2 * kOwnTile; }
+constexpr size_t kOwnSmem = kOwnWarps * own_ring_bytes(kOwnStages);
+
+__device__ __forceinline__ void cp_async16_zero(uint32_t smem, const void* g, bool valid) {
+  const int n = valid ? 16 : 0;  // 0: the 16 bytes are filled with zeros, nothing is read
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem), "l"(g), "r"(n)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm_x4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm_x4_t(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ int live_len(const ri_token_cache& c, int unit, int* status) {
+  int len = c.lens[unit];
+  if (len < 0 || len > c.capacity) {
+    record_status(status, RI_ERR_INVALID_ARG);
+    len = len < 0 ? 0 : c.capacity;
+  }
+  return len;
+}
+
+template <int kStages>
+__device__ __forceinline__ void own_task(const AttendParams& p, int task, uint32_t buf) {
+  const int unit = task / p.splits, split = task - unit * p.splits;
+  const int G = p.c.group_size, Gp = G <= 4 ? 4 : 8;
+  const int lane = threadIdx.x & 31;
+  const int g = lane >> 2, tq = lane & 3;  // score row (query) and column pair of a thread
+  const int cap = p.c.capacity;
+  const int len = live_len(p.c, unit, p.status);
+  // whole tiles of 16 tokens, split evenly
+  const int tiles = (len + kOwnTokens - 1) / kOwnTokens;
+  const int t0 = (int)((long long)tiles * split / p.splits);
+  const int t1 = (int)((long long)tiles * (split + 1) / p.splits);
+  float* ml = p.ml + ((size_t)unit * p.splits + split) * G * 2;
+  if (t0 >= t1) {
+    if (lane < G) *reinterpret_cast<float2*>(ml + lane * 2) = make_float2(-INFINITY, 0.f);
+    return;
+  }
+  const uint8_t* K = static_cast<const uint8_t*>(p.c.K) + (size_t)unit * cap * kD * 2;
+  const uint8_t* V = static_cast<const uint8_t*>(p.c.V) + (size_t)unit * cap * kD * 2;
+
+  // chunk c (16 bytes) of row r of a tile, XOR-swizzled for ldmatrix
+  auto at = [](int r, int c) { return (uint32_t)(r * 256 + ((c ^ (r & 7)) << 4)); };
+  auto copy = [&](int t, int stage) {
+    const uint32_t dst = buf + stage * 2 * kOwnTile;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {  // two whole rows per instruction
+      const int r = 2 * i + (lane >> 4), c = lane & 15;
+      const int tok = t * kOwnTokens + r;
+      const bool valid = tok < len;
+      const size_t src = valid ? (size_t)tok * 256 + c * 16 : 0;
+      cp_async16_zero(dst + at(r, c), K + src, valid);
+      cp_async16_zero(dst + kOwnTile + at(r, c), V + src, valid);
+    }
+  };
+  __syncwarp();  // the ring's last readers (the warp's task before) are through
+#pragma unroll
+  for (int i = 0; i < kStages - 1; ++i) {
+    if (t0 + i < t1) copy(t0 + i, i);
+    cp_async_commit();
+  }
+  // query rows as the A operand: rows g (valid below G), rows 8..15 are zero
+  uint32_t qa[8][2];
+  const uint32_t* q = reinterpret_cast<const uint32_t*>(
+      p.q + ((size_t)unit * G + (g < G ? g : 0)) * kD);
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    qa[k][0] = g < G ? q[k * 8 + tq] : 0u;
+    qa[k][1] = g < G ? q[k * 8 + 4 + tq] : 0u;
+  }
+  float m = -INFINITY, l = 0.f;  // of query g, over this thread's columns for l
+  float o[8][4];                 // numerator^T: rows d = 16 i + lane / 4 (+ 8), columns 2 tq, + 1
+#pragma unroll
+  for (int i = 0; i < 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+
+  int stage = 0;
+#pragma unroll 1
+  for (int t = t0; t < t1; ++t) {
+    if (t + kStages - 1 < t1)
+      copy(t + kStages - 1, stage == 0 ? kStages - 1 : stage - 1);
+    cp_async_commit();
+    cp_async_wait<kStages - 1>();
+    __syncwarp();
+    const uint32_t kb = buf + stage * 2 * kOwnTile, vb = kb + kOwnTile;
+    float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      // matrices: keys 0-7 / 8-15 (lane bit 4) x the two halves of 16 d (bit 3)
+      uint32_t b[4];
+      ldsm_x4(b, kb + at((lane & 7) + ((lane >> 4) << 3), 2 * k + ((lane >> 3) & 1)));
+      mma16816(s[0], qa[k][0], 0u, qa[k][1], 0u, b[0], b[1]);
+      mma16816(s[1], qa[k][0], 0u, qa[k][1], 0u, b[2], b[3]);
+    }
+    float x[4] = {s[0][0] * kScaleLog2, s[0][1] * kScaleLog2, s[1][0] * kScaleLog2,
+                  s[1][1] * kScaleLog2};
+    const int tok = t * kOwnTokens + 2 * tq;  // tokens tok, tok + 1, tok + 8, tok + 9
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int ti = tok + (i & 1) + (i >> 1) * 8;
+      if (ti >= len) x[i] = -INFINITY;
+      else if (p.add_weight && g < G) p.score[((size_t)unit * cap + ti) * Gp + g] = x[i];
+    }
+    float top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+    top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
+    top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));  // finite: a tile has a valid token
+    const bool grow = top > m + kLazy;
+    if (__any_sync(~0u, grow)) {
+      const float mn = grow ? top : m;
+      const float f = m == -INFINITY ? 0.f : exp2_approx(m - mn);
+      m = mn;
+      l *= f;
+      const float f0 = __shfl_sync(~0u, f, 8 * tq), f1 = __shfl_sync(~0u, f, 8 * tq + 4);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        o[i][0] *= f0;
+        o[i][1] *= f1;
+        o[i][2] *= f0;
+        o[i][3] *= f1;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = exp2_approx(x[i] - m);
+    l += (x[0] + x[1]) + (x[2] + x[3]);
+    const uint32_t p0 = pack_bf16(x[0], x[1]), p1 = pack_bf16(x[2], x[3]);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      // V^T: matrices keys 0-7 / 8-15 (lane bit 4) x d halves of 16 (bit 3)
+      uint32_t a[4];
+      ldsm_x4_t(a, vb + at((lane & 7) + ((lane >> 4) << 3), 2 * i + ((lane >> 3) & 1)));
+      mma16816(o[i], a[0], a[1], a[2], a[3], p0, p1);
+    }
+    __syncwarp();
+    stage = stage + 1 == kStages ? 0 : stage + 1;
+  }
+  l += __shfl_xor_sync(~0u, l, 1);
+  l += __shfl_xor_sync(~0u, l, 2);
+  if (tq == 0 && g < G) *reinterpret_cast<float2*>(ml + g * 2) = make_float2(m, l);
+  float* num = p.num + ((size_t)unit * p.splits + split) * G * kD;
+#pragma unroll
+  for (int e = 0; e < 2; ++e)
+    if (2 * tq + e < G)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        num[(2 * tq + e) * kD + 16 * i + g] = o[i][e];
+        num[(2 * tq + e) * kD + 16 * i + g + 8] = o[i][2 + e];
+      }
+}
+
+// Tasks [.., tasks) from the shared counter, one at a time; every task's
+// result is the same whoever takes it.
+__device__ __forceinline__ int take_task(const AttendParams& p) {
+  int t = 0;
+  if ((threadIdx.x & 31) == 0) t = atomicAdd(p.next_task, 1);
+  return __shfl_sync(~0u, t, 0);
+}
+
+// The own tokens without a prefix, or what the warps beside the prefix have
+// left of them: those blocks start as the prefix's blocks end.
+__global__ void __launch_bounds__(kOwnThreads)
+    own_kernel(const __grid_constant__ AttendParams p) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int warp = threadIdx.x >> 5;
+  const uint32_t buf = smem_u32(smem) + warp * own_ring_bytes(kOwnStages);
+  if (p.plan.blocks) {
+    for (int t = take_task(p); t < p.tasks; t = take_task(p)) own_task<kOwnStages>(p, t, buf);
+  } else {
+    for (int t = blockIdx.x * kOwnWarps + warp; t < p.tasks; t += gridDim.x * kOwnWarps)
+      own_task<kOwnStages>(p, t, buf);
+  }
+  // this launch completes after the prefix launch, so that the merge, which
+  // waits for this one, has both
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 // ------------------------------------------------------------ prefix kernel
-constexpr int kRing = 5;                  // K / V tiles in flight
+constexpr int kRing = 4;                  // K / V tiles in flight
 constexpr int kSoftmaxWarps = 8;          // two warpgroups, one per slot
 constexpr int kWarpMma = 8, kWarpLoad = 9;
-constexpr int kPrefixThreads = 384;       // warps 10 and 11 fill the third warpgroup
+constexpr int kWarpOwn = 10;              // warps 10 and 11: own tokens meanwhile
+constexpr int kPrefixThreads = 384;
 // Registers: 168 per thread at launch (384 x 168 = 64512); the softmax
-// warpgroups hold a row's 128 scores and take 200 each, the third goes down
-// to 96: 256 x 200 + 128 x 96 = 63488.
-constexpr int kRegsSoftmax = 200, kRegsRest = 96;
+// warpgroups hold a row's 128 scores and take 192 each, the third goes down
+// to 112: 256 x 192 + 128 x 112 = 63488.
+constexpr int kRegsSoftmax = 192, kRegsRest = 112;
 // TMEM columns: scores (and, over them, the probabilities) of slot i, then
 // the numerators
 constexpr uint32_t kColS = 0, kColO = 256;
-constexpr float kLazy = 8.f;  // log2: the reference moves when the maximum passes it by this
 
 struct PrefixShared {
   uint64_t full[kRing], empty[kRing];
   uint64_t q_full, s_full[2], p_full[2], o_full[2], drain;
   uint32_t tmem;
+  int done;  // the block's prefix work is through: no more own shares are taken
 };
-constexpr size_t kPrefixSmem = 1024 + (2 + kRing) * (size_t)kTileBytes + sizeof(PrefixShared);
+constexpr size_t kPrefixSmem = 1024 + (2 + kRing) * (size_t)kTileBytes +
+                               2 * own_ring_bytes(kOwnStagesBeside) + sizeof(PrefixShared);
 
 // V tile [key][d] as the B operand of num += P V (N = d contiguous, "MN
 // major"): 128-byte swizzle, 64 columns of d per half tile; adjacent halves
@@ -244,7 +462,7 @@ struct Share {
   bool pair;
 };
 
-__device__ __forceinline__ Share share_of(const PrefixPlan& p, int u, long long x0, long long x1) {
+__device__ __forceinline__ Share share_of(const PrefixPlan& p, int u, int x0, int x1) {
   Share s;
   s.head = u / p.per_head;
   s.row0 = (u % p.per_head) * 2 * kTile;
@@ -262,7 +480,9 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~1023ull);
   uint8_t* sq = base;                       // 2 query tiles
   uint8_t* ring = base + 2 * kTileBytes;    // kRing K / V tiles
-  PrefixShared* sh = reinterpret_cast<PrefixShared*>(ring + kRing * kTileBytes);
+  uint8_t* own = ring + kRing * kTileBytes; // the rings of warps 10 and 11
+  PrefixShared* sh =
+      reinterpret_cast<PrefixShared*>(own + 2 * own_ring_bytes(kOwnStagesBeside));
   // (shuffled: uniform over the warp for the compiler too)
   const int tid = threadIdx.x, warp = __shfl_sync(~0u, tid >> 5, 0), lane = tid & 31;
   const PrefixPlan& plan = p.plan;
@@ -284,6 +504,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
       mbar_init(&sh->o_full[i], 1);
     }
     mbar_init(&sh->drain, 1);
+    sh->done = 0;
     fence_barrier_init();
   }
   tc_fence_before();
@@ -291,7 +512,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(~0u, sh->tmem, 0);
 
-  const long long x0 = plan.from(blockIdx.x), x1 = plan.from(blockIdx.x + 1);
+  const int x0 = plan.from(blockIdx.x), x1 = plan.from(blockIdx.x + 1);
   const int u0 = plan.unit_of(x0);
   const int last_tile = plan.key_tiles - 1;
   // A wait that expires is recorded once; its role then runs on without
@@ -448,6 +669,15 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
         if (!mbar_wait(&sh->drain, 0)) record_status(p.status, RI_ERR_TIMEOUT);
       }
       __syncwarp();
+    } else {
+      // ------------------------------------------ own tokens, meanwhile
+      const uint32_t buf = smem_u32(own) + (warp - kWarpOwn) * own_ring_bytes(kOwnStagesBeside);
+      while (!*reinterpret_cast<volatile int*>(&sh->done)) {
+        const int t = take_task(p);
+        if (t >= p.tasks) break;
+        own_task<kOwnStagesBeside>(p, t, buf);
+      }
+      cp_async_wait<0>();
     }
   } else {
     // ----------------------------------------------------------- softmax
@@ -572,46 +802,63 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
         wait(&sh->o_full[slot], o_phase);
         o_phase ^= 1;
       }
+      // Through shared memory (the query tiles are free: 8 KB per warp), so
+      // that rows leave as whole 256-byte pieces: a thread holds a row, and 32
+      // rows' 16-byte stores would each touch 32 lines.
       const size_t out_slot = 2 * ((size_t)blockIdx.x + u) + (s.pair ? slot : 0);
       float* num = p.pnum + out_slot * kTile * kD;
       float* ml = p.pml + out_slot * kTile * 2;
-      const bool row_ok = row_tile0 + row < plan.rows;
+      uint8_t* stage = sq + warp * 8192;
+      const int warp_row = (warp & 3) * 32;
+      const int n_rows = min(32, plan.rows - row_tile0 - warp_row);  // <= 0: none live
+      auto put = [&](int i, uint4 v) {  // 16-byte chunk i of this thread's row
+        *reinterpret_cast<uint4*>(stage + lane * 256 + ((i ^ (lane & 15)) << 4)) = v;
+      };
+      auto send = [&](int half) {  // 64 columns of the warp's rows
+        __syncwarp();
+        for (int r = lane >> 4; r < n_rows; r += 2)
+          *reinterpret_cast<uint4*>(num + (warp_row + r) * kD + half * 64 + (lane & 15) * 4) =
+              *reinterpret_cast<const uint4*>(stage + r * 256 + (((lane & 15) ^ (r & 15)) << 4));
+        __syncwarp();
+      };
       if (s.pair) {
+        named_barrier(1, kSoftmaxWarps * 32);  // both slots' scores are through
         if (ok && live) {
           tc_fence_after();
-          if (row_ok) *reinterpret_cast<float2*>(ml + row * 2) = make_float2(m, l);
+          if (lane < n_rows) *reinterpret_cast<float2*>(ml + row * 2) = make_float2(m, l);
 #pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
-            uint32_t o[32];
-            tmem_ld32_nowait(t_o + c * 32, o);
+          for (int half = 0; half < 2; ++half) {
+            uint32_t a[32], b[32];
+            tmem_ld32_nowait(t_o + half * 64, a);
+            tmem_ld32_nowait(t_o + half * 64 + 32, b);
             tmem_wait_ld();
-            if (row_ok)
 #pragma unroll
-              for (int i = 0; i < 8; ++i)
-                *reinterpret_cast<uint4*>(num + ((c * 8 + i) * kTile + row) * 4) =
-                    make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+            for (int i = 0; i < 8; ++i) {
+              put(i, make_uint4(a[4 * i], a[4 * i + 1], a[4 * i + 2], a[4 * i + 3]));
+              put(8 + i, make_uint4(b[4 * i], b[4 * i + 1], b[4 * i + 2], b[4 * i + 3]));
+            }
+            send(half);
           }
           tc_fence_before();
         }
       } else {
-        // both slots hold the same rows: (m, l) change hands in the second
-        // query tile, which is free here, and each warpgroup joins half of the
-        // columns of both numerators
+        // both slots hold the same rows: (m, l) change hands, and each
+        // warpgroup joins half of the columns of both numerators
         float2* ex = reinterpret_cast<float2*>(sq + kTileBytes);  // [2][128]
         ex[slot * kTile + row] = used ? make_float2(m, l) : make_float2(-INFINITY, 0.f);
         named_barrier(1, kSoftmaxWarps * 32);
         const float2 e0 = ex[row], e1 = ex[kTile + row];
-        const float m0 = e0.x, l0 = e0.y, m1 = e1.x, l1 = e1.y;
-        const float M = fmaxf(m0, m1);
-        const float f0 = exp2_approx(m0 - M), f1 = exp2_approx(m1 - M);
+        named_barrier(1, kSoftmaxWarps * 32);
+        const float M = fmaxf(e0.x, e1.x);
+        const float f0 = exp2_approx(e0.x - M), f1 = exp2_approx(e1.x - M);
         const bool both = s.t1 - s.t0 > 1;
         if (ok && live) {
           tc_fence_after();
-          if (row_ok && slot == 0)
-            *reinterpret_cast<float2*>(ml + row * 2) = make_float2(M, f0 * l0 + f1 * l1);
-          const uint32_t t_num = tmem + lane_addr + kColO;
+          if (lane < n_rows && slot == 0)
+            *reinterpret_cast<float2*>(ml + row * 2) = make_float2(M, f0 * e0.y + f1 * e1.y);
+          const uint32_t t_num = tmem + lane_addr + kColO + slot * 64;
 #pragma unroll 1
-          for (int c = 2 * slot; c < 2 * slot + 2; ++c) {
+          for (int c = 0; c < 2; ++c) {
             uint32_t a[32], b[32];
             tmem_ld32_nowait(t_num + c * 32, a);
             if (both) tmem_ld32_nowait(t_num + kD + c * 32, b);
@@ -622,12 +869,11 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
               if (both) v = fmaf(f1, __uint_as_float(b[i]), v);
               a[i] = __float_as_uint(v);
             }
-            if (row_ok)
 #pragma unroll
-              for (int i = 0; i < 8; ++i)
-                *reinterpret_cast<uint4*>(num + ((c * 8 + i) * kTile + row) * 4) =
-                    make_uint4(a[4 * i], a[4 * i + 1], a[4 * i + 2], a[4 * i + 3]);
+            for (int i = 0; i < 8; ++i)
+              put(c * 8 + i, make_uint4(a[4 * i], a[4 * i + 1], a[4 * i + 2], a[4 * i + 3]));
           }
+          send(slot);
           tc_fence_before();
         }
       }
@@ -635,250 +881,55 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
       // scores were waited for) before the next unit replaces either
       named_barrier(1, kSoftmaxWarps * 32);
     }
+    if (tid == 0) *reinterpret_cast<volatile int*>(&sh->done) = 1;
   }
   tc_fence_before();
   __syncthreads();
   if (warp == kWarpMma) tmem_dealloc(tmem, 512);
 }
 
-// --------------------------------------------------------------- own tokens
-// One block of four warps per (sequence, KV head, share); the share's tiles
-// of 16 tokens are dealt to the warps, each with its own ring of copies.
-constexpr int kOwnWarps = 4;
-constexpr int kOwnThreads = kOwnWarps * 32;
-constexpr int kOwnTokens = 16;
-constexpr int kOwnRing = 3;
-constexpr int kOwnTile = kOwnTokens * kD * 2;  // 4 KB of K, as much of V
-constexpr size_t kOwnSmem = (size_t)kOwnWarps * kOwnRing * 2 * kOwnTile;
-
-__device__ __forceinline__ void cp_async16_zero(uint32_t smem, const void* g, bool valid) {
-  const int n = valid ? 16 : 0;  // 0: the 16 bytes are filled with zeros, nothing is read
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem), "l"(g), "r"(n)
-               : "memory");
-}
-__device__ __forceinline__ void ldsm_x4(uint32_t (&r)[4], uint32_t addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
-}
-__device__ __forceinline__ void ldsm_x4_t(uint32_t (&r)[4], uint32_t addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
-}
-__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                         uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-      "{%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-__device__ __forceinline__ int live_len(const ri_token_cache& c, int unit, int* status) {
-  int len = c.lens[unit];
-  if (len < 0 || len > c.capacity) {
-    if (threadIdx.x == 0) record_status(status, RI_ERR_INVALID_ARG);
-    len = len < 0 ? 0 : c.capacity;
-  }
-  return len;
-}
-
-__global__ void __launch_bounds__(kOwnThreads) own_kernel(const __grid_constant__ AttendParams p) {
-  extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ float sh_m[kOwnWarps][8], sh_l[kOwnWarps][8];
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int unit = blockIdx.x / p.splits, split = blockIdx.x % p.splits;
-  const int G = p.c.group_size, Gp = G <= 4 ? 4 : 8;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int g = lane >> 2, tq = lane & 3;  // score row (query) and column pair of a thread
-  const int cap = p.c.capacity;
-  const int len = live_len(p.c, unit, p.status);
-  // whole tiles of 16 tokens, split evenly
-  const int tiles = (len + kOwnTokens - 1) / kOwnTokens;
-  const int t0 = (int)((long long)tiles * split / p.splits);
-  const int t1 = (int)((long long)tiles * (split + 1) / p.splits);
-  const uint8_t* K = static_cast<const uint8_t*>(p.c.K) + (size_t)unit * cap * kD * 2;
-  const uint8_t* V = static_cast<const uint8_t*>(p.c.V) + (size_t)unit * cap * kD * 2;
-  const uint32_t buf = smem_u32(smem) + warp * kOwnRing * 2 * kOwnTile;
-
-  // chunk c (16 bytes) of row r of a tile, XOR-swizzled for ldmatrix
-  auto at = [](int r, int c) { return (uint32_t)(r * 256 + ((c ^ (r & 7)) << 4)); };
-  auto copy = [&](int t, int stage) {
-    const uint32_t dst = buf + stage * 2 * kOwnTile;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {  // two whole rows per instruction
-      const int r = 2 * i + (lane >> 4), c = lane & 15;
-      const int tok = t * kOwnTokens + r;
-      const bool valid = tok < len;
-      const size_t src = valid ? (size_t)tok * 256 + c * 16 : 0;
-      cp_async16_zero(dst + at(r, c), K + src, valid);
-      cp_async16_zero(dst + kOwnTile + at(r, c), V + src, valid);
-    }
-  };
-#pragma unroll
-  for (int i = 0; i < kOwnRing - 1; ++i) {
-    if (t0 + warp + i * kOwnWarps < t1) copy(t0 + warp + i * kOwnWarps, i);
-    cp_async_commit();
-  }
-  // query rows as the A operand: rows g (valid below G), rows 8..15 are zero
-  uint32_t qa[8][2];
-  const uint32_t* q = reinterpret_cast<const uint32_t*>(
-      p.q + ((size_t)unit * G + (g < G ? g : 0)) * kD);
-#pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    qa[k][0] = g < G ? q[k * 8 + tq] : 0u;
-    qa[k][1] = g < G ? q[k * 8 + 4 + tq] : 0u;
-  }
-  float m = -INFINITY, l = 0.f;  // of query g, over this thread's columns for l
-  float o[8][4];                 // numerator^T: rows d = 16 i + lane / 4 (+ 8), columns 2 tq, + 1
-#pragma unroll
-  for (int i = 0; i < 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-
-  int stage = 0;
-  for (int t = t0 + warp; t < t1; t += kOwnWarps) {
-    const int ahead = t + (kOwnRing - 1) * kOwnWarps;
-    if (ahead < t1) copy(ahead, (stage + kOwnRing - 1) % kOwnRing);
-    cp_async_commit();
-    cp_async_wait<kOwnRing - 1>();
-    __syncwarp();
-    const uint32_t kb = buf + stage * 2 * kOwnTile, vb = kb + kOwnTile;
-    float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      // matrices: keys 0-7 / 8-15 (lane bit 4) x the two halves of 16 d (bit 3)
-      uint32_t b[4];
-      ldsm_x4(b, kb + at((lane & 7) + ((lane >> 4) << 3), 2 * k + ((lane >> 3) & 1)));
-      mma16816(s[0], qa[k][0], 0u, qa[k][1], 0u, b[0], b[1]);
-      mma16816(s[1], qa[k][0], 0u, qa[k][1], 0u, b[2], b[3]);
-    }
-    float x[4] = {s[0][0] * kScaleLog2, s[0][1] * kScaleLog2, s[1][0] * kScaleLog2,
-                  s[1][1] * kScaleLog2};
-    const int tok = t * kOwnTokens + 2 * tq;  // tokens tok, tok + 1, tok + 8, tok + 9
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int ti = tok + (i & 1) + (i >> 1) * 8;
-      if (ti >= len) x[i] = -INFINITY;
-      else if (p.add_weight && g < G) p.score[((size_t)unit * cap + ti) * Gp + g] = x[i];
-    }
-    float top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
-    top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
-    top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));  // finite: a tile has a valid token
-    const bool grow = top > m + kLazy;
-    if (__any_sync(~0u, grow)) {
-      const float mn = grow ? top : m;
-      const float f = m == -INFINITY ? 0.f : exp2_approx(m - mn);
-      m = mn;
-      l *= f;
-      const float f0 = __shfl_sync(~0u, f, 8 * tq), f1 = __shfl_sync(~0u, f, 8 * tq + 4);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        o[i][0] *= f0;
-        o[i][1] *= f1;
-        o[i][2] *= f0;
-        o[i][3] *= f1;
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] = exp2_approx(x[i] - m);
-    l += (x[0] + x[1]) + (x[2] + x[3]);
-    const uint32_t p0 = pack_bf16(x[0], x[1]), p1 = pack_bf16(x[2], x[3]);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      // V^T: matrices keys 0-7 / 8-15 (lane bit 4) x d halves of 16 (bit 3)
-      uint32_t a[4];
-      ldsm_x4_t(a, vb + at((lane & 7) + ((lane >> 4) << 3), 2 * i + ((lane >> 3) & 1)));
-      mma16816(o[i], a[0], a[1], a[2], a[3], p0, p1);
-    }
-    __syncwarp();
-    stage = (stage + 1) % kOwnRing;
-  }
-  cp_async_wait<0>();
-  l += __shfl_xor_sync(~0u, l, 1);
-  l += __shfl_xor_sync(~0u, l, 2);
-  if (tq == 0) {
-    sh_m[warp][g] = m;
-    sh_l[warp][g] = l;
-  }
-  __syncthreads();  // also: every warp is done with its ring, which now takes numerators
-  float* num = reinterpret_cast<float*>(smem);  // [warp][query][128]
-#pragma unroll
-  for (int i = 0; i < 8; ++i)
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      num[(warp * 8 + 2 * tq + (e & 1)) * kD + 16 * i + g + (e >> 1) * 8] = o[i][e];
-  __syncthreads();
-  for (int r = 0; r < G; ++r) {
-    float M = -INFINITY, sum = 0.f, acc = 0.f;
-#pragma unroll
-    for (int w = 0; w < kOwnWarps; ++w) M = fmaxf(M, sh_m[w][r]);
-    if (M > -INFINITY) {
-#pragma unroll
-      for (int w = 0; w < kOwnWarps; ++w) {
-        const float f = exp2_approx(sh_m[w][r] - M);
-        sum += f * sh_l[w][r];
-        acc += f * num[(w * 8 + r) * kD + threadIdx.x];
-      }
-    }
-    const size_t i = ((size_t)unit * p.splits + split) * G + r;
-    p.num[i * kD + threadIdx.x] = acc;
-    if (threadIdx.x == 0) *reinterpret_cast<float2*>(p.ml + i * 2) = make_float2(M, sum);
-  }
-  // this launch completes after the prefix launch, so that the merge, which
-  // waits for this one, has both
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-}
-
 // -------------------------------------------------------------------- merge
 // One block per (sequence, KV head) and chunk of its own tokens.  Every block
 // joins the references and sums of its G rows (a warp per row, its lanes over
-// the shares); the first one also joins the numerators, four rows at a time,
-// with the shares' factors in shared memory.
-constexpr int kMergeThreads = 512;
+// the shares, whose factors 2^(m - M) stay in shared memory); the unit's
+// blocks share out the rows' numerators, four columns per lane.
+constexpr int kMergeThreads = 256;
+constexpr int kMergeTokens = 4 * kMergeThreads;  // own tokens of a chunk
 
 __global__ void __launch_bounds__(kMergeThreads)
     merge_kernel(const __grid_constant__ AttendParams p, int chunks) {
-  extern __shared__ float factor[];  // [G][shares]: reference, then 2^(m - M)
+  extern __shared__ float factor[];  // [G][shares]
   __shared__ float sh_lse[kMaxGroup], sh_l[kMaxGroup];
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int unit = blockIdx.x / chunks, chunk = blockIdx.x % chunks;
+  __shared__ int sh_n[kMaxGroup], sh_slot[kMaxGroup];  // prefix shares, the first one's slot
+  __shared__ float4 sh_part[kMergeThreads / 32][32];
+  const int unit = blockIdx.x / chunks, chunk = blockIdx.x - unit * chunks;
   const int G = p.c.group_size, H = p.c.num_kv_heads, Gp = G <= 4 ? 4 : 8;
-  const int b = unit / H, h = unit % H;
+  const int b = unit / H, h = unit - b * H;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int len = live_len(p.c, unit, p.status);
   const PrefixPlan& plan = p.plan;
   const int shares = plan.blocks + p.splits;  // room per row; most rows use fewer
-  // A row's prefix shares come from blocks c0 .. c1 - 1 (the G rows of a
-  // sequence may lie in two row tiles, even in two units).
-  auto unit_of_row = [&](int r) { return h * plan.per_head + r / (2 * kTile); };
-  auto block_range = [&](int u, int* c0, int* c1) {
-    *c0 = *c1 = 0;
-    if (!plan.blocks) return;
-    const long long s0 = plan.start(u);
-    const long long s1 = s0 + (long long)plan.work_per_tile(u) * plan.key_tiles;
-    *c0 = (int)(s0 * plan.blocks / plan.total);
-    const int e = (int)((s1 * plan.blocks + plan.total - 1) / plan.total);
-    *c1 = e < plan.blocks ? e : plan.blocks;
-  };
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (blockIdx.x == 0 && threadIdx.x == 0) *p.next_task = 0;  // every task has been taken
+  const int len = live_len(p.c, unit, p.status);
   if (warp < G) {
-    const int g = warp, r = b * G + g;
-    const int u = plan.blocks ? unit_of_row(r) : 0;
-    int c0, c1;
-    block_range(u, &c0, &c1);
-    const int second = r / kTile & 1, pr = r % kTile;
-    const int n_prefix = c1 - c0;
-    float* f = factor + (size_t)g * shares;
+    const int g = warp, r = b * G + g, row = r % kTile;
+    int c0 = 0, n_prefix = 0, u = 0, slot = 0;
+    if (plan.blocks) {
+      // the blocks whose work meets the row's unit
+      u = h * plan.per_head + r / (2 * kTile);
+      const int s0 = plan.start(u), s1 = s0 + plan.work_per_tile(u) * plan.key_tiles;
+      c0 = s0 / plan.chunk;
+      n_prefix = (s1 + plan.chunk - 1) / plan.chunk - c0;
+      slot = 2 * (c0 + u) + (r / kTile & 1);
+    }
+    float* f = factor + g * shares;
     float m = -INFINITY, l = 0.f;
     for (int i = lane; i < n_prefix + p.splits; i += 32) {
       float2 v = make_float2(-INFINITY, 0.f);
       if (i < n_prefix) {
-        const int c = c0 + i;
         // (a block on the unit's edge may have no tile of it)
-        if (plan.tile_at(u, plan.from(c)) < plan.tile_at(u, plan.from(c + 1)))
-          v = *reinterpret_cast<const float2*>(
-              p.pml + ((2 * ((size_t)c + u) + second) * kTile + pr) * 2);
+        if (plan.tile_at(u, plan.from(c0 + i)) < plan.tile_at(u, plan.from(c0 + i + 1)))
+          v = *reinterpret_cast<const float2*>(p.pml + ((size_t)(slot + 2 * i) * kTile + row) * 2);
       } else {
         v = *reinterpret_cast<const float2*>(
             p.ml + (((size_t)unit * p.splits + i - n_prefix) * G + g) * 2);
@@ -902,49 +953,78 @@ __global__ void __launch_bounds__(kMergeThreads)
     if (lane == 0) {
       sh_l[g] = l;
       sh_lse[g] = l > 0.f ? M + log2f(l) : -INFINITY;
+      sh_n[g] = n_prefix;
+      sh_slot[g] = slot;
     }
   }
   __syncthreads();
-  if (chunk == 0) {
-    const int d = threadIdx.x & 127;
-    for (int g = threadIdx.x >> 7; g < G; g += kMergeThreads / 128) {
-      const int r = b * G + g;
-      const int u = plan.blocks ? unit_of_row(r) : 0;
-      int c0, c1;
-      block_range(u, &c0, &c1);
-      const float* f = factor + (size_t)g * shares;
-      const float* src = p.pnum + 2 * ((size_t)c0 + u) * kTile * kD +
-                         (size_t)(r / kTile & 1) * kTile * kD +
-                         ((d >> 2) * kTile + r % kTile) * 4 + (d & 3);
-      const int n = c1 - c0;
-      float acc = 0.f;
-#pragma unroll 8
-      for (int i = 0; i < n; ++i) {
-        const float w = f[i];  // 0: the share was not written
-        if (w > 0.f) acc = fmaf(w, src[(size_t)i * 2 * kTile * kD], acc);
+  // The numerators: row g is joined by block g mod chunks of the unit, by
+  // `per_row` warps that take its shares in turn, eight loads in flight each.
+  const int rows_here = chunk < G ? (G - chunk + chunks - 1) / chunks : 0;
+  if (rows_here) {
+    const int per_row = rows_here <= 1 ? 8 : rows_here <= 2 ? 4 : rows_here <= 4 ? 2 : 1;
+    const int g = chunk + warp / per_row * chunks, part = warp % per_row;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (g < G) {
+      const int n = sh_n[g], all = n + p.splits;
+      const float* f = factor + g * shares;
+      const float4* prefix = reinterpret_cast<const float4*>(p.pnum) +
+                             ((size_t)sh_slot[g] * kTile + (b * G + g) % kTile) * (kD / 4) + lane;
+      const float4* own = reinterpret_cast<const float4*>(p.num) +
+                          ((size_t)unit * p.splits * G + g) * (kD / 4) + lane;
+      for (int i0 = part; i0 < all; i0 += 8 * per_row) {
+        float4 v[8];
+        float w[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int i = i0 + j * per_row;
+          w[j] = i < all ? f[i] : 0.f;
+          v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+          // factor 0: nothing was written there, or nothing that counts
+          if (w[j] > 0.f)
+            v[j] = *(i < n ? prefix + (size_t)i * 2 * kTile * (kD / 4)
+                           : own + (size_t)(i - n) * G * (kD / 4));
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          acc.x = fmaf(w[j], v[j].x, acc.x);
+          acc.y = fmaf(w[j], v[j].y, acc.y);
+          acc.z = fmaf(w[j], v[j].z, acc.z);
+          acc.w = fmaf(w[j], v[j].w, acc.w);
+        }
       }
-      const float* own = p.num + ((size_t)unit * p.splits * G + g) * kD + d;
-#pragma unroll 4
-      for (int i = 0; i < p.splits; ++i) {
-        const float w = f[n + i];
-        acc = fmaf(w, own[(size_t)i * G * kD], acc);
-      }
-      const float l = sh_l[g];
+    }
+    if (per_row > 1) {
+      sh_part[warp][lane] = acc;
+      __syncthreads();
+      if (part == 0)
+        for (int i = 1; i < per_row; ++i) {
+          const float4 v = sh_part[warp + i][lane];
+          acc.x += v.x;
+          acc.y += v.y;
+          acc.z += v.z;
+          acc.w += v.w;
+        }
+    }
+    if (g < G && part == 0) {
+      const float l = sh_l[g], inv = l > 0.f ? 1.f / l : 0.f;
       const size_t row = (size_t)unit * G + g;
-      p.out[row * kD + d] = __float2bfloat16_rn(l > 0.f ? acc / l : 0.f);
-      if (p.lse && d == 0) p.lse[row] = sh_lse[g] * kLn2;
+      *reinterpret_cast<uint2*>(p.out + row * kD + lane * 4) =
+          make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+      if (p.lse && lane == 0) p.lse[row] = sh_lse[g] * kLn2;
     }
   }
   if (!p.add_weight) return;
   float lse[kMaxGroup];
 #pragma unroll
   for (int g = 0; g < kMaxGroup; ++g) lse[g] = g < G ? sh_lse[g] : 0.f;
-  for (int i = chunk * kMergeThreads + threadIdx.x; i < len; i += chunks * kMergeThreads) {
+  const int end = min(len, (chunk + 1) * kMergeTokens);
+#pragma unroll 4
+  for (int i = chunk * kMergeTokens + threadIdx.x; i < end; i += kMergeThreads) {
     const size_t row = (size_t)unit * p.c.capacity + i;
     const float4* s = reinterpret_cast<const float4*>(p.score + row * Gp);
-    float w = 0.f;
     const float4 a = s[0];
-    w += exp2_approx(a.x - lse[0]);
+    float w = exp2_approx(a.x - lse[0]);
     if (G > 1) w += exp2_approx(a.y - lse[1]);
     if (G > 2) w += exp2_approx(a.z - lse[2]);
     if (G > 3) w += exp2_approx(a.w - lse[3]);
@@ -1015,13 +1095,15 @@ cudaError_t launch_dependent(void (*kernel)(Args...), int blocks, int threads, s
 }  // namespace
 
 size_t token_attend_bytes(const ri_token_cache& c, int prefix_len) {
-  return layout(c, plan_prefix(c, prefix_len)).total;
+  PrefixPlan plan;
+  if (!plan_prefix(c, prefix_len, &plan)) return 0;
+  return layout(c, plan).total;
 }
 
 cudaError_t launch_token_attend(const TokenAttendArgs& a, cudaStream_t s) {
   AttendParams p;
   memset(&p, 0, sizeof(p));
-  p.plan = plan_prefix(a.c, a.p.length);
+  if (!plan_prefix(a.c, a.p.length, &p.plan)) return cudaErrorInvalidValue;
   const AttendLayout L = layout(a.c, p.plan);
   p.c = a.c;
   p.q = static_cast<const __nv_bfloat16*>(a.q);
@@ -1033,8 +1115,11 @@ cudaError_t launch_token_attend(const TokenAttendArgs& a, cudaStream_t s) {
   p.num = reinterpret_cast<float*>(a.ws + L.off_num);
   p.score = reinterpret_cast<float*>(a.ws + L.off_score);
   p.status = reinterpret_cast<int*>(a.ws);
+  p.next_task = reinterpret_cast<int*>(a.ws + kTaskCounter);
   p.prefix_len = a.p.length;
   p.splits = L.splits;
+  const int units = a.c.batch * a.c.num_kv_heads;
+  p.tasks = units * L.splits;
   p.add_weight = a.add_weight;
   cudaError_t e = set_smem_once(5, reinterpret_cast<const void*>(own_kernel), (int)kOwnSmem);
   if (e != cudaSuccess) return e;
@@ -1047,16 +1132,20 @@ cudaError_t launch_token_attend(const TokenAttendArgs& a, cudaStream_t s) {
     prefix_kernel<<<p.plan.blocks, kPrefixThreads, kPrefixSmem, s>>>(mk, mv, p);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
-  const int units = a.c.batch * a.c.num_kv_heads;
   // The prefix launch is ordered like any other; the two after it may start
   // while it runs (programmatic dependent launch): the own tokens' blocks
-  // share nothing with it and fill the SMs it leaves, the merge waits for both.
-  e = launch_dependent(own_kernel, units * L.splits, kOwnThreads, kOwnSmem, s, p.plan.blocks > 0,
-                       p);
-  if (e != cudaSuccess) return e;
-  const int chunks = a.add_weight ? (a.c.capacity + 2 * kMergeThreads - 1) / (2 * kMergeThreads) : 1;
-  const size_t smem = (size_t)a.c.group_size * (p.plan.blocks + L.splits) * sizeof(float);
-  return launch_dependent(merge_kernel, units * chunks, kMergeThreads, smem, s, true, p, chunks);
+  // take the SMs that it leaves, the merge waits for both.
+  const int fill = 2 * num_sms(), want = (p.tasks + kOwnWarps - 1) / kOwnWarps;
+  e = launch_dependent(own_kernel, want < fill ? want : fill, kOwnThreads, kOwnSmem, s,
+                       p.plan.blocks > 0, p);
+  if (e == cudaSuccess) {
+    const int chunks = a.add_weight ? (a.c.capacity + kMergeTokens - 1) / kMergeTokens : 1;
+    const size_t smem = (size_t)a.c.group_size * (p.plan.blocks + L.splits) * sizeof(float);
+    e = launch_dependent(merge_kernel, units * chunks, kMergeThreads, smem, s, true, p, chunks);
+  }
+  // without its merge a prefix launch leaves the counter standing
+  if (e != cudaSuccess && p.plan.blocks) cudaMemsetAsync(p.next_task, 0, sizeof(int), s);
+  return e;
 }
 
 }  // namespace ri
