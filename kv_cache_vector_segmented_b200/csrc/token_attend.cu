@@ -153,6 +153,29 @@ __device__ __forceinline__ float exp2_approx(float x) {
   return y;
 }
 
+// Two fp32 operations in one instruction.
+struct f2 {
+  unsigned long long v;
+};
+__device__ __forceinline__ f2 make_f2(float lo, float hi) {
+  f2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void split(f2 a, float* lo, float* hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(*lo), "=f"(*hi) : "l"(a.v));
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+  f2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+  f2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -390,7 +413,7 @@ constexpr uint32_t kColS = 0, kColO = 256;
 
 struct PrefixShared {
   uint64_t full[kRing], empty[kRing];
-  uint64_t q_full, s_full[2], p_full[2], o_full[2], drain;
+  uint64_t q_full, s_full[2], p_full[2][2], o_full[2], drain;
   uint32_t tmem;
   int done;  // the block's prefix work is through: no more own shares are taken
 };
@@ -500,7 +523,8 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
     mbar_init(&sh->q_full, kSoftmaxWarps * 32);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh->s_full[i], 1);
-      mbar_init(&sh->p_full[i], 4);
+      mbar_init(&sh->p_full[i][0], 4);
+      mbar_init(&sh->p_full[i][1], 4);
       mbar_init(&sh->o_full[i], 1);
     }
     mbar_init(&sh->drain, 1);
@@ -595,18 +619,25 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
           }
           __syncwarp();
         };
-        // O[slot] += P[slot] V
+        // O[slot] += P[slot] V, the first 64 keys while the others are in the works
         auto values = [&](int slot, int i, bool first) {
-          if (!ok) return;
-          tc_fence_after();
           const uint64_t b = umma_desc_v(ring_addr + (i % kRing) * kTileBytes);
           const uint32_t d = tmem + kColO + slot * kD, a = tmem + kColS + slot * kTile;
-          if (elect_one()) {
-            umma_ts(d, a, b, idesc_o, !first);
+          const uint32_t phase = (p_phases >> slot) & 1;
+          p_phases ^= 1u << slot;
+          wait_tile(i);
 #pragma unroll
-            for (int k = 1; k < 8; ++k) umma_ts(d, a + 8 * k, b + k * (2048 >> 4), idesc_o, 1);
+          for (int half = 0; half < 2; ++half) {
+            wait(&sh->p_full[slot][half], phase);
+            if (!ok) return;
+            tc_fence_after();
+            if (elect_one()) {
+#pragma unroll
+              for (int k = 4 * half; k < 4 * half + 4; ++k)
+                umma_ts(d, a + 8 * k, b + k * (2048 >> 4), idesc_o, k > 0 || !first);
+            }
+            __syncwarp();
           }
-          __syncwarp();
         };
         auto release = [&](int i) { commit(&sh->empty[i % kRing]); };
         for (int u = u0; u < plan.units && plan.start(u) < x1; ++u) {
@@ -625,9 +656,6 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
               const int k = j + 1 < T ? n++ : -1;
 #pragma unroll 1
               for (int slot = 0; slot < 2; ++slot) {
-                wait(&sh->p_full[slot], (p_phases >> slot) & 1);
-                p_phases ^= 1u << slot;
-                if (slot == 0) wait_tile(v);
                 values(slot, v, j == 0);
                 if (slot == 1) release(v);
                 if (k >= 0) {
@@ -649,9 +677,6 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
               const int slot = j & 1;
               const int v = n++;
               const int k = j + 2 < T ? n++ : -1;
-              wait(&sh->p_full[slot], (p_phases >> slot) & 1);
-              p_phases ^= 1u << slot;
-              wait_tile(v);
               values(slot, v, j < 2);
               release(v);
               if (k >= 0) {
@@ -774,26 +799,39 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
             }
           }
           any = true;
-          float sum[4] = {0.f, 0.f, 0.f, 0.f};
+          const f2 scale = make_f2(kScaleLog2, kScaleLog2), shift = make_f2(-m, -m);
+          f2 sum[2] = {make_f2(0.f, 0.f), make_f2(0.f, 0.f)};
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             uint32_t pk[16];
 #pragma unroll
-            for (int i = 0; i < 32; i += 2) {
-              const float a = exp2_approx(fmaf(__uint_as_float(x[c][i]), kScaleLog2, -m));
-              const float b = exp2_approx(fmaf(__uint_as_float(x[c][i + 1]), kScaleLog2, -m));
-              sum[i & 2] += a;
-              sum[(i & 2) + 1] += b;
-              pk[i >> 1] = pack_bf16(a, b);
+            for (int i = 0; i < 16; ++i) {
+              const f2 v = fma2(make_f2(__uint_as_float(x[c][2 * i]), __uint_as_float(x[c][2 * i + 1])),
+                          scale, shift);
+              float a, b;
+              split(v, &a, &b);
+              a = exp2_approx(a);
+              b = exp2_approx(b);
+              sum[i & 1] = add2(sum[i & 1], make_f2(a, b));
+              pk[i] = pack_bf16(a, b);
             }
             tmem_st16(t_s + c * 16, pk);
+            if (c & 1) {  // 64 keys are through: their products may start
+              tmem_wait_st();
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&sh->p_full[slot][c >> 1]);
+            }
           }
-          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-          tmem_wait_st();
-          tc_fence_before();
+          float s0, s1, s2, s3;
+          split(sum[0], &s0, &s1);
+          split(sum[1], &s2, &s3);
+          l += (s0 + s1) + (s2 + s3);
+        } else if (lane == 0) {
+          mbar_arrive(&sh->p_full[slot][0]);
+          mbar_arrive(&sh->p_full[slot][1]);
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sh->p_full[slot]);
       }
 
       // -------------------------------------------- the unit's share goes out
