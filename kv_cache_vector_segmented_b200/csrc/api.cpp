@@ -40,7 +40,21 @@ namespace {
 constexpr int kMaxDevicesHost = 64;
 std::mutex g_smem_mu;
 bool g_smem_done[kMaxDevicesHost][kSmemSlots];
+bool g_cluster_done[kMaxDevicesHost][kSmemSlots];
 }  // namespace
+
+cudaError_t allow_large_clusters(int slot, const void* func) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= kMaxDevicesHost || slot < 0 || slot >= kSmemSlots)
+    return cudaErrorInvalidValue;
+  std::lock_guard<std::mutex> lk(g_smem_mu);
+  if (g_cluster_done[dev][slot]) return cudaSuccess;
+  e = cudaFuncSetAttribute(func, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e == cudaSuccess) g_cluster_done[dev][slot] = true;
+  return e;
+}
 
 cudaError_t set_smem_once(int slot, const void* func, int bytes) {
   int dev = 0;

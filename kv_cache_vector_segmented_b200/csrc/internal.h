@@ -261,5 +261,7 @@ int num_sms();
 // kernel in a fixed table (kSmemSlots entries).
 constexpr int kSmemSlots = 16;
 cudaError_t set_smem_once(int slot, const void* func, int bytes);
+// Allows a kernel clusters of more than 8 blocks, once per device; same slots.
+cudaError_t allow_large_clusters(int slot, const void* func);
 
 }  // namespace ri
