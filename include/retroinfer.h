@@ -701,7 +701,7 @@ size_t ri_token_evict_workspace(const ri_token_cache* cache, int32_t budget);
  *          that is shared must have the same capacity, others must not
  *          overlap.  Rows from the new length on are left as they were.
  * budget >= 1, keep_first >= 0, keep_recent >= 0, keep_first + keep_recent
- * <= budget. */
+ * <= budget; cache capacity <= 2^24 (RI_ERR_UNSUPPORTED above). */
 ri_status ri_token_evict(const ri_token_cache* cache, int32_t budget, int32_t keep_first,
                          int32_t keep_recent, const ri_token_cache* out, void* workspace,
                          size_t workspace_bytes, ri_stream_t stream);

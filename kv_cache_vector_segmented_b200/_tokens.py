@@ -211,7 +211,7 @@ class TokenCache:
         self._c = CTokenCache(B, H, group_size, d, cap, K.data_ptr(), V.data_ptr(),
                               pos.data_ptr(), weight.data_ptr(), lens.data_ptr())
         self._ref = ctypes.byref(self._c)
-        token_evict_workspace_bytes(self, 1)  # the library's checks of the sizes
+        token_attend_workspace_bytes(self, 0)  # the library's checks of the sizes
         self.status = alloc_workspace(256, dev)
 
     @classmethod

@@ -236,6 +236,7 @@ struct TokenEvictArgs {
   int budget, keep_first, keep_recent;
   char* ws;
 };
+constexpr int kEvictMaxCapacity = 1 << 24;  // a bit per row of a block's slice in shared memory
 size_t token_evict_bytes(const ri_token_cache& c, int budget);
 cudaError_t launch_token_evict(const TokenEvictArgs& a, cudaStream_t s);
 

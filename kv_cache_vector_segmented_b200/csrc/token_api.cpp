@@ -262,6 +262,11 @@ size_t ri_token_evict_workspace(const ri_token_cache* cache, int32_t budget) {
     set_error("budget must be >= 1 (got %d)", budget);
     return 0;
   }
+  if (cache->capacity > kEvictMaxCapacity) {
+    set_error("eviction handles capacities up to %d (got %d)", kEvictMaxCapacity,
+              cache->capacity);
+    return 0;
+  }
   return token_evict_bytes(*cache, budget);
 }
 
@@ -281,6 +286,8 @@ ri_status ri_token_evict(const ri_token_cache* cache, int32_t budget, int32_t ke
   const int W = budget < cache->capacity ? budget : cache->capacity;
   RI_CHECK(out->capacity >= W, RI_ERR_CAPACITY, "out holds %d tokens, %d needed", out->capacity,
            W);
+  RI_CHECK(cache->capacity <= kEvictMaxCapacity, RI_ERR_UNSUPPORTED,
+           "eviction handles capacities up to %d (got %d)", kEvictMaxCapacity, cache->capacity);
   const size_t units = (size_t)cache->batch * cache->num_kv_heads;
   const size_t n = units * cache->capacity, m = units * out->capacity;
   const struct { const void *a, *b; size_t size; const char* name; } pairs[] = {

@@ -4,16 +4,19 @@
 //
 // The order is total: held tokens (first and most recent positions) before
 // all others, then larger weight, then lower row.  A token's rank is a 32-bit
-// key (the order-preserving image of its weight, all ones when held), so the
-// keep-th largest key is found by four 8-bit digits (radix selection), and
-// ties on it are settled by counting in row order.  Every step is a count or
-// a prefix sum: the result does not depend on the order in which threads run.
+// key (the order-preserving image of its weight, all ones when held).  The
+// keep-th token is found by counting: the keys' range is cut into 512 equal
+// buckets, the bucket that holds the keep-th key is cut again while it has
+// more than 512 keys (once in all is usual: a float's bits spread the weights
+// over the range by their logarithm), and its keys are then ranked one
+// against the other.  Every step is a count, a prefix sum or a comparison:
+// the result does not depend on the order in which threads run.
 //
 // One thread-block cluster per (sequence, KV head), one launch.  A block
 // holds a contiguous slice of the rows' keys in shared memory (read once);
-// the blocks add up their digit counts through distributed shared memory,
-// with one cluster barrier per digit.  Bound: reading 8 bytes per token and
-// moving 2 x 512 bytes per token that changes its row.
+// blocks exchange counts and candidates through distributed shared memory.
+// Bound: reading 8 bytes per token and moving 2 x 512 bytes per token that
+// changes its row.
 #include "common.cuh"
 #include "internal.h"
 
@@ -44,14 +47,22 @@ __device__ __forceinline__ uint32_t rank_key(float w, int pos, int first, long l
   return float_order_key(w + 0.f);
 }
 
+constexpr int kBuckets = kThreads;  // one thread sums one bucket
+constexpr int kPasses = 4;          // 9 bits each, of 32
+constexpr int kRanked = kThreads;   // most candidates ranked directly
+
 // Shared memory every block of a cluster may read.
 struct Exchange {
-  int hist[4][256];  // counts of one digit each
+  int hist[kPasses][kBuckets];
+  unsigned long long mine[kRanked], all[kRanked];  // candidates: key, then ~row
+  int n_mine;
   int newest;
-  int ties;          // rows of the threshold key in this slice
-  int holes, moved;  // of this slice
-  int total[256];
-  int digit, above, count;
+  uint32_t low, high;  // raw keys of the slice
+  int held;
+  int ties, cut;       // mass ties of the slice; the last kept row among them
+  int holes, moved;    // of this slice
+  int bucket, above, count;
+  uint32_t cut_key;
   int warp_a[kWarps], warp_b[kWarps];
 };
 
@@ -61,6 +72,21 @@ __device__ __forceinline__ int remote_int(const int* p, int rank) {
   asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
   asm volatile("ld.shared::cluster.b32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
   return v;
+}
+
+__device__ __forceinline__ unsigned long long remote_u64(const unsigned long long* p, int rank) {
+  uint32_t a;
+  unsigned long long v;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.b64 %0, [%1];" : "=l"(v) : "r"(a) : "memory");
+  return v;
+}
+
+// Lane b's copy of a word of block b of the unit (0 from lane n on), so that
+// all blocks' words arrive in one round trip.
+__device__ __forceinline__ int gather_int(const int* p, int n) {
+  const int lane = threadIdx.x & 31;
+  return lane < n ? remote_int(p, lane) : 0;
 }
 
 // Barrier over the unit's blocks (one: the block's own).
@@ -91,8 +117,9 @@ __device__ __forceinline__ int warps_before(int count, int* sums, int* all) {
 
 // kHeld: the slice's keys stay in shared memory.
 template <bool kHeld>
-__global__ void __launch_bounds__(kThreads) evict_kernel(const __grid_constant__ EvictParams p) {
-  extern __shared__ uint32_t held[];  // keys, then positions, of the slice
+__global__ void __launch_bounds__(kThreads, 2) evict_kernel(const __grid_constant__ EvictParams p) {
+  // kHeld: the slice's keys, its positions; then one bit per row
+  extern __shared__ uint32_t held[];
   __shared__ Exchange x;
   const int n_blocks = p.cluster;
   const int unit = blockIdx.x / n_blocks, rank = blockIdx.x - unit * n_blocks;
@@ -112,127 +139,210 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const __grid_constant__
   const float* weight = p.c.weight + (size_t)unit * cap;
   uint32_t* keys = held;
   uint32_t* poss = held + slice;
+  uint32_t* bits = kHeld ? poss + slice : held;
   const bool leaves = keep < len;
 
-  int need_ties = 0;
-  uint32_t key = 0;
+  // a row's token stays: its key is above cut_key, or equal and not behind cut_row
+  uint32_t cut_key = 0;
+  int cut_row = INT_MAX;
   long long recent_from = 0;
   auto key_of = [&](int i) {  // row r0 + i
     return kHeld ? keys[i] : rank_key(weight[r0 + i], pos[r0 + i], p.first, recent_from);
   };
-  if (leaves) {
-    // ---- the newest position, over the unit
-    int newest = INT_MIN;
-    for (int i = tid; i < rows; i += kThreads) {
-      const int q = pos[r0 + i];
-      if (kHeld) {
-        poss[i] = (uint32_t)q;
-        keys[i] = __float_as_uint(weight[r0 + i]);
-      }
-      newest = max(newest, q);
-    }
-    for (int i = tid; i < 4 * 256; i += kThreads) (&x.hist[0][0])[i] = 0;
-    if (tid == 0) x.newest = INT_MIN;
-    __syncthreads();
-    newest = __reduce_max_sync(~0u, newest);
-    if (lane == 0) atomicMax(&x.newest, newest);
-    unit_sync(n_blocks);
-    newest = INT_MIN;
-    for (int b = 0; b < n_blocks; ++b) newest = max(newest, remote_int(&x.newest, b));
-    recent_from = (long long)newest - p.recent;
-
-    // ---- the keep-th largest key, digit by digit from the top
-    uint32_t mask = 0;
-    int above = 0, count = 0;  // keys above the prefix; keys of it
-#pragma unroll 1
-    for (int d = 0; d < 4; ++d) {
-      const int shift = 24 - 8 * d;
-      for (int i = tid; i < rows; i += kThreads) {
-        uint32_t k;
-        if (kHeld && d == 0) {
-          k = rank_key(__uint_as_float(keys[i]), (int)poss[i], p.first, recent_from);
-          keys[i] = k;
-        } else {
-          k = key_of(i);
-        }
-        if ((k & mask) == key) atomicAdd(&x.hist[d][(k >> shift) & 255], 1);
-      }
-      unit_sync(n_blocks);
-      if (tid < 256) {
-        int sum = 0;
-        for (int b = 0; b < n_blocks; ++b) sum += remote_int(&x.hist[d][tid], b);
-        x.total[255 - tid] = sum;  // largest digit first
-      }
-      __syncthreads();
-      if (warp == 0) {
-        int v[8], mine = 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) mine += v[i] = x.total[8 * lane + i];
-        int upto = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int y = __shfl_up_sync(~0u, upto, o);
-          if (lane >= o) upto += y;
-        }
-        int before = above + upto - mine;
-        if (before < keep && keep <= before + mine) {  // one lane: the digit is among its 8
-          int i = 0;
-          while (before + v[i] < keep) before += v[i++];
-          x.digit = 255 - (8 * lane + i);
-          x.above = before;
-          x.count = v[i];
-        }
-      }
-      __syncthreads();
-      key |= (uint32_t)x.digit << shift;
-      mask |= 255u << shift;
-      above = x.above;
-      count = x.count;
-    }
-    need_ties = keep - above;  // rows of that key kept, in row order
-    if (need_ties == count) need_ties = INT_MAX;  // all of them: no counting
-  }
-
   // A warp takes 32 * steps rows in a row, so ranks come from ballots.
   const int steps = (rows + kThreads - 1) / kThreads;
   const int w0 = warp * 32 * steps;  // first row of the warp in the slice
   auto row_in = [&](int s) { return w0 + 32 * s + lane; };
-  int tie_base = 0;
-  if (leaves && need_ties != INT_MAX) {
-    int n = 0;
-    for (int s = 0; s < steps; ++s) {
-      const int i = row_in(s);
-      n += __popc(__ballot_sync(~0u, i < rows && key_of(i) == key));
+  if (leaves) {
+    // ---- the newest position and the keys' range, over the unit
+    for (int i = tid; i < kPasses * kBuckets; i += kThreads) (&x.hist[0][0])[i] = 0;
+    if (tid == 0) {
+      x.newest = INT_MIN;
+      x.low = 0xFFFFFFFFu;
+      x.high = 0;
+      x.n_mine = x.held = 0;
+      x.cut = -1;
     }
-    int all;
-    tie_base = warps_before(n, x.warp_a, &all);
-    if (tid == 0) x.ties = all;
+    int newest = INT_MIN;
+    uint32_t low = 0xFFFFFFFFu, high = 0;
+#pragma unroll 8
+    for (int i = tid; i < rows; i += kThreads) {
+      const int q = pos[r0 + i];
+      const uint32_t k = rank_key(weight[r0 + i], 0, 0, 0);  // as if not held
+      if (kHeld) {
+        poss[i] = (uint32_t)q;
+        keys[i] = k;
+      }
+      newest = max(newest, q);
+      low = min(low, k);
+      high = max(high, k);
+    }
+    newest = __reduce_max_sync(~0u, newest);
+    low = __reduce_min_sync(~0u, low);
+    high = __reduce_max_sync(~0u, high);
+    __syncthreads();
+    if (lane == 0) {
+      atomicMax(&x.newest, newest);
+      atomicMin(&x.low, low);
+      atomicMax(&x.high, high);
+    }
     unit_sync(n_blocks);
-    for (int b = 0; b < rank; ++b) tie_base += remote_int(&x.ties, b);
+    {
+      const int a = gather_int(&x.newest, n_blocks);
+      const uint32_t b = (uint32_t)gather_int(reinterpret_cast<int*>(&x.low), n_blocks);
+      const uint32_t c = (uint32_t)gather_int(reinterpret_cast<int*>(&x.high), n_blocks);
+      newest = __reduce_max_sync(~0u, lane < n_blocks ? a : INT_MIN);
+      low = __reduce_min_sync(~0u, lane < n_blocks ? b : 0xFFFFFFFFu);
+      high = __reduce_max_sync(~0u, lane < n_blocks ? c : 0u);
+    }
+    recent_from = (long long)newest - p.recent;
+
+    // ---- the bucket of the keep-th key, narrowed down
+    const uint32_t span = high - low;
+    int shift = span < kBuckets ? 0 : 32 - __clz(span) - 9;  // span >> shift < 512
+    uint32_t range = span;  // keys of interest: low .. low + range
+    int above = 0, count = 0;
+#pragma unroll 1
+    for (int pass = 0;; ++pass) {
+      int held_mine = 0;
+      for (int i = tid; i < rows; i += kThreads) {
+        uint32_t k;
+        if (kHeld && pass == 0) {
+          const int q = (int)poss[i];
+          k = q < p.first || q > recent_from ? 0xFFFFFFFFu : keys[i];
+          keys[i] = k;
+        } else {
+          k = key_of(i);
+        }
+        if (k == 0xFFFFFFFFu) ++held_mine;
+        else if (k >= low && k - low <= range) atomicAdd(&x.hist[pass][(k - low) >> shift], 1);
+      }
+      if (pass == 0) {
+        held_mine = __reduce_add_sync(~0u, held_mine);
+        if (lane == 0 && held_mine) atomicAdd(&x.held, held_mine);
+      }
+      unit_sync(n_blocks);
+      if (pass == 0) above = __reduce_add_sync(~0u, gather_int(&x.held, n_blocks));
+      if (above >= keep) {  // the held ones alone are enough
+        count = INT_MAX;
+        low = 0xFFFFFFFFu;
+        above = 0;
+        break;
+      }
+      // thread t sums bucket 511 - t, so that a prefix sum runs from the top
+      int v[kMaxCluster], sum = 0;
+#pragma unroll
+      for (int b = 0; b < kMaxCluster; ++b)
+        v[b] = b < n_blocks ? remote_int(&x.hist[pass][kBuckets - 1 - tid], b) : 0;
+#pragma unroll
+      for (int b = 0; b < kMaxCluster; ++b) sum += v[b];
+      int upto = sum;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(~0u, upto, o);
+        if (lane >= o) upto += y;
+      }
+      int all;
+      const int warp_total = __shfl_sync(~0u, upto, 31);
+      const int before = above + warps_before(warp_total, x.warp_a, &all) + upto - sum;
+      if (before < keep && keep <= before + sum) {  // one thread of the block
+        x.bucket = kBuckets - 1 - tid;
+        x.above = before;
+        x.count = sum;
+      }
+      __syncthreads();
+      low += (uint32_t)x.bucket << shift;
+      above = x.above;
+      count = x.count;
+      range = (1u << shift) - 1;  // of this bucket
+      if (count <= kRanked || shift == 0) break;
+      shift = shift > 9 ? shift - 9 : 0;
+    }
+    const int need = keep - above;  // of the bucket's keys, in order
+
+    if (count <= kRanked) {
+      // ---- the bucket's keys are ranked one against the other
+      for (int i = tid; i < rows; i += kThreads) {
+        const uint32_t k = key_of(i);
+        if (k != 0xFFFFFFFFu && k >= low && k - low <= range)
+          x.mine[atomicAdd(&x.n_mine, 1)] = (unsigned long long)k << 32 | (uint32_t)~(r0 + i);
+      }
+      unit_sync(n_blocks);
+      int n = gather_int(&x.n_mine, n_blocks), first = 0;  // lane b: block b's
+      for (int b = 0; b < n_blocks; ++b) {
+        const int nb = __shfl_sync(~0u, n, b);
+        for (int i = tid; i < nb; i += kThreads) x.all[first + i] = remote_u64(&x.mine[i], b);
+        first += nb;
+      }
+      __syncthreads();
+      if (tid < count) {
+        const unsigned long long me = x.all[tid];
+        int larger = 0;
+#pragma unroll 4
+        for (int j = 0; j < count; ++j) larger += x.all[j] > me;
+        if (larger == need - 1) {
+          x.cut_key = (uint32_t)(me >> 32);
+          x.above = (int)~(uint32_t)me;  // its row
+        }
+      }
+      __syncthreads();
+      cut_key = x.cut_key;
+      cut_row = x.above;
+    } else {
+      // ---- many rows of one key: the need-th of them, in row order
+      cut_key = low;
+      int n = 0;
+      for (int s = 0; s < steps; ++s) {
+        const int i = row_in(s);
+        n += __popc(__ballot_sync(~0u, i < rows && key_of(i) == cut_key));
+      }
+      int all;
+      int t = warps_before(n, x.warp_b, &all);
+      if (tid == 0) x.ties = all;
+      unit_sync(n_blocks);
+      t += __reduce_add_sync(~0u, gather_int(&x.ties, rank));
+      for (int s = 0; s < steps; ++s) {
+        const int i = row_in(s);
+        const uint32_t m = __ballot_sync(~0u, i < rows && key_of(i) == cut_key);
+        if ((m >> lane & 1) && t + __popc(m & ((1u << lane) - 1)) == need - 1) x.cut = r0 + i;
+        t += __popc(m);
+      }
+      unit_sync(n_blocks);
+      const int c = gather_int(&x.cut, n_blocks);
+      cut_row = __reduce_max_sync(~0u, lane < n_blocks ? c : -1);
+    }
   }
-  // the row's token stays; `t` counts the ties met by the warp
-  auto kept_row = [&](int i, int* t) {
-    if (!leaves) return i < rows;
-    const uint32_t k = i < rows ? key_of(i) : 0u;
-    bool kept = i < rows && k > key;
-    const bool tie = i < rows && k == key;
-    const uint32_t ties = __ballot_sync(~0u, tie);
-    if (tie) kept = tie_base + *t + __popc(ties & ((1u << lane) - 1)) < need_ties;
-    *t += __popc(ties);
-    return kept;
+  auto kept_key = [&](int i) {
+    const uint32_t k = key_of(i);
+    return k > cut_key || (k == cut_key && r0 + i <= cut_row);
   };
 
+  // K or V of the result in another array: rows that stay are copied as well,
+  // listed behind the moves (a row's rank among them: the rows below it that
+  // are no holes)
+  const bool kv_apart = p.c.K != p.o.K || p.c.V != p.o.V;
   int n_moves = 0;
   int32_t* holes = p.holes + (size_t)unit * W;
   int32_t* moved = p.moved + (size_t)unit * W;
   if (leaves) {
-    // ---- ranks of the holes below keep and of the kept rows from keep on
-    int t = 0, nh = 0, nm = 0;
+    // ---- one bit per row: its token stays; holes below keep and kept rows
+    // from keep on are counted per warp, then ranked
+    auto masks = [&](int i0, uint32_t kept, uint32_t* hole, uint32_t* move) {
+      const int low = min(max(keep - (r0 + i0), 0), 32);  // the word's rows below keep
+      const uint32_t below = low == 32 ? ~0u : (1u << low) - 1;
+      *hole = below & ~kept;  // (keep <= len: rows below keep are all live)
+      *move = ~below & kept;
+    };
+    uint32_t hole, move;
+    int nh = 0, nm = 0;
     for (int s = 0; s < steps; ++s) {
-      const int i = row_in(s), r = r0 + i;
-      const bool kept = kept_row(i, &t);
-      nh += __popc(__ballot_sync(~0u, i < rows && r < keep && !kept));
-      nm += __popc(__ballot_sync(~0u, r >= keep && kept));
+      const int i = row_in(s), i0 = w0 + 32 * s;
+      if (i0 >= rows) break;  // uniform over the warp
+      const uint32_t kept = __ballot_sync(~0u, i < rows && kept_key(i));
+      if (lane == 0) bits[i0 >> 5] = kept;
+      masks(i0, kept, &hole, &move);
+      nh += __popc(hole);
+      nm += __popc(move);
     }
     int all_h, all_m;
     int h = warps_before(nh, x.warp_a, &all_h), m = warps_before(nm, x.warp_b, &all_m);
@@ -241,89 +351,76 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const __grid_constant__
       x.moved = all_m;
     }
     unit_sync(n_blocks);
-    for (int b = 0; b < n_blocks; ++b) {
-      const int bh = remote_int(&x.holes, b), bm = remote_int(&x.moved, b);
-      if (b < rank) {
-        h += bh;
-        m += bm;
-      }
-      n_moves += bh;
-    }
-    t = 0;
+    const int bh = gather_int(&x.holes, n_blocks), bm = gather_int(&x.moved, n_blocks);
+    n_moves = __reduce_add_sync(~0u, bh);
+    h += __reduce_add_sync(~0u, lane < rank ? bh : 0);
+    m += __reduce_add_sync(~0u, lane < rank ? bm : 0);
+    const uint32_t lt = (1u << lane) - 1;
     for (int s = 0; s < steps; ++s) {
-      const int i = row_in(s), r = r0 + i;
-      const bool kept = kept_row(i, &t);
-      const bool hole = i < rows && r < keep && !kept, move = r >= keep && kept;
-      const uint32_t bh = __ballot_sync(~0u, hole), bm = __ballot_sync(~0u, move);
-      const uint32_t lt = (1u << lane) - 1;
-      if (hole) holes[h + __popc(bh & lt)] = r;
-      if (move) moved[m + __popc(bm & lt)] = r;
-      h += __popc(bh);
-      m += __popc(bm);
+      const int i0 = w0 + 32 * s, r = r0 + i0 + lane;
+      if (i0 >= rows) break;
+      masks(i0, bits[i0 >> 5], &hole, &move);
+      const int hb = h + __popc(hole & lt);
+      if (hole >> lane & 1) holes[hb] = r;
+      else if (move >> lane & 1) moved[m + __popc(move & lt)] = r;
+      else if (kv_apart && r < keep) holes[n_moves + r - hb] = moved[n_moves + r - hb] = r;
+      h += __popc(hole);
+      m += __popc(move);
     }
+    __syncthreads();  // bits of other warps are read below
   }
-  // the lists are complete, nothing reads the old state by rank from here on,
-  // and no block's shared memory is read any more
+  // the lists are complete, nothing ranks by the old state from here on, and
+  // no block's shared memory is read any more
   unit_sync(n_blocks);
   if (rank == 0 && tid == 0) p.o.lens[unit] = keep;
 
   const size_t src0 = (size_t)unit * cap, dst0 = (size_t)unit * p.o.capacity;
-  const uint4* kv_src = reinterpret_cast<const uint4*>(lane < 16 ? p.c.K : p.c.V);
-  uint4* kv_dst = reinterpret_cast<uint4*>(lane < 16 ? p.o.K : p.o.V);
-  const int ch = lane & 15;
-  // ---- kept rows below keep, where an array of the result is another one
-  const bool kv_apart = kv_src != kv_dst, any_kv = __any_sync(~0u, kv_apart);
   const bool pos_apart = p.c.pos != p.o.pos, weight_apart = p.c.weight != p.o.weight;
-  if (any_kv || pos_apart || weight_apart) {
-    int t = 0;
-    for (int s = 0; s < steps; ++s) {
-      if (r0 + w0 + 32 * s >= keep) break;  // uniform over the warp
-      const int i = row_in(s), r = r0 + i;
-      const bool stays = kept_row(i, &t) && r < keep;
-      if (stays && pos_apart) p.o.pos[dst0 + r] = pos[r];
-      if (stays && weight_apart) p.o.weight[dst0 + r] = weight[r];
-      uint32_t left = any_kv ? __ballot_sync(~0u, stays) : 0u;
-      while (left) {
-        uint4 v[4];
-        int row[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          row[j] = -1;
-          if (left) {
-            row[j] = r0 + w0 + 32 * s + __ffs(left) - 1;
-            left &= left - 1;
-          }
-          if (row[j] >= 0 && kv_apart) v[j] = kv_src[(src0 + row[j]) * 16 + ch];
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (row[j] >= 0 && kv_apart) kv_dst[(dst0 + row[j]) * 16 + ch] = v[j];
+  // ---- positions and weights of rows that stay, where only these are apart
+  if (!kv_apart && (pos_apart || weight_apart)) {
+    const int end = min(rows, keep - r0);
+#pragma unroll 4
+    for (int i = tid; i < end; i += kThreads) {
+      const int q = pos[r0 + i];
+      const float f = weight[r0 + i];
+      if (!leaves || (bits[i >> 5] >> (i & 31) & 1)) {
+        p.o.pos[dst0 + r0 + i] = q;
+        p.o.weight[dst0 + r0 + i] = f;
       }
     }
   }
-  // (keys read from memory again must not meet a moved token's)
-  if (!kHeld) unit_sync(n_blocks);
-  // ---- moved[k] -> holes[k], four rows in flight per warp.  Sources lie at
-  // or behind keep, destinations before it: no move reads what another writes.
+  // ---- row moved[k] -> row holes[k]: a warp takes up to 32 in a row, their
+  // numbers in one load, their K and V eight rows in flight.  Sources of moves
+  // lie at or behind keep, destinations before it: no move reads what another
+  // writes.
+  const uint4* kv_src = reinterpret_cast<const uint4*>(lane < 16 ? p.c.K : p.c.V);
+  uint4* kv_dst = reinterpret_cast<uint4*>(lane < 16 ? p.o.K : p.o.V);
+  const int ch = lane & 15;
   const int warps = n_blocks * kWarps;
-  for (int k0 = rank * kWarps + warp; k0 < n_moves; k0 += 4 * warps) {
+  // (nothing leaves: the rows are their own list)
+  const int n_rows = kv_apart ? keep : n_moves;
+  const int run = min(32, (n_rows + warps - 1) / warps);
+  for (int k0 = (rank * kWarps + warp) * run; k0 < n_rows; k0 += warps * run) {
+    const int n = min(run, n_rows - k0);
     int from = 0, to = 0;
-    if (lane < 4 && k0 + lane * warps < n_moves) {
-      from = moved[k0 + lane * warps];
-      to = holes[k0 + lane * warps];
-      p.o.pos[dst0 + to] = pos[from];
-      p.o.weight[dst0 + to] = weight[from];
+    if (lane < n) {
+      from = leaves ? moved[k0 + lane] : k0 + lane;
+      to = leaves ? holes[k0 + lane] : k0 + lane;
+      if (from != to || pos_apart) p.o.pos[dst0 + to] = pos[from];
+      if (from != to || weight_apart) p.o.weight[dst0 + to] = weight[from];
     }
-    uint4 v[4];
+    for (int j0 = 0; j0 < n; j0 += 8) {
+      uint4 v[8];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int f = __shfl_sync(~0u, from, j);
-      if (k0 + j * warps < n_moves) v[j] = kv_src[(src0 + f) * 16 + ch];
-    }
+      for (int j = 0; j < 8; ++j) {
+        const int f = __shfl_sync(~0u, from, j0 + j);
+        if (j0 + j < n) v[j] = kv_src[(src0 + f) * 16 + ch];
+      }
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int d = __shfl_sync(~0u, to, j);
-      if (k0 + j * warps < n_moves) kv_dst[(dst0 + d) * 16 + ch] = v[j];
+      for (int j = 0; j < 8; ++j) {
+        const int d = __shfl_sync(~0u, to, j0 + j);
+        if (j0 + j < n) kv_dst[(dst0 + d) * 16 + ch] = v[j];
+      }
     }
   }
 }
@@ -359,7 +456,11 @@ cudaError_t launch_token_evict(const TokenEvictArgs& a, cudaStream_t s) {
   const int slice = ((cap + cluster - 1) / cluster + 31) & ~31;
   const bool held = slice <= kMaxHeld;
   void (*kernel)(EvictParams) = held ? evict_kernel<true> : evict_kernel<false>;
-  cudaError_t e = set_smem_once(6, reinterpret_cast<const void*>(evict_kernel<true>), kMaxHeld * 8);
+  cudaError_t e = set_smem_once(6, reinterpret_cast<const void*>(evict_kernel<true>),
+                                kMaxHeld * 8 + kMaxHeld / 8);
+  if (e == cudaSuccess)
+    e = set_smem_once(7, reinterpret_cast<const void*>(evict_kernel<false>),
+                      kEvictMaxCapacity / kMaxCluster / 8 + 4);
   if (e == cudaSuccess)
     e = allow_large_clusters(6, reinterpret_cast<const void*>(evict_kernel<true>));
   if (e == cudaSuccess)
@@ -368,7 +469,7 @@ cudaError_t launch_token_evict(const TokenEvictArgs& a, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(units * cluster));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = held ? (size_t)slice * 8 : 0;
+  cfg.dynamicSmemBytes = (held ? (size_t)slice * 8 : 0) + slice / 8;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;

@@ -483,6 +483,12 @@ def test_evict_long(R):
     _evict_case(R, 1, 1, 40000, [40000], 39000, 4, 64, "self")
 
 
+@pytest.mark.parametrize("into", ["self", "shared", "other"])
+def test_evict_longer_than_shared_memory(R, into):
+    """A slice too long to be held: its keys are read from memory each time."""
+    _evict_case(R, 1, 1, 400000, [399000], 30000, 4, 64, into, edit=_ties)
+
+
 def test_evict_bad_lengths_reported(R):
     c = _random_cache(R, 1, 4, 1, 30, [0] * 4, 1, poison=False)
     c.lens.copy_(torch.tensor([[-3, 31, 2 ** 31 - 1, 4]], dtype=torch.int32))

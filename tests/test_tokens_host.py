@@ -135,6 +135,9 @@ def test_size_limits(R, C):
     assert lib.ri_token_attend_workspace(b(_cache(C, capacity=(1 << 28) + 1)), 0) == 0
     assert lib.ri_token_attend_workspace(b(_cache(C)), -1) == 0
     assert lib.ri_token_evict_workspace(b(_cache(C)), 0) == 0
+    big = _cache(C, capacity=(1 << 24) + 1)
+    assert lib.ri_token_evict_workspace(b(big), 8) == 0
+    assert lib.ri_token_evict(b(big), 8, 0, 0, b(big), PTR, 1 << 30, None) == UNSUPPORTED
     assert lib.ri_token_attend(b(_cache(C, batch=65537, num_kv_heads=1)), PTR, None, PTR, None, 1,
                                PTR, 1 << 30, None) == UNSUPPORTED
 
