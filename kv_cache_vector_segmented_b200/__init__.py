@@ -31,10 +31,9 @@ __all__ = list(_EXPORTS + _TOKEN_EXPORTS)
 
 
 def __getattr__(name):
-    if name in _EXPORTS:
-        binding = importlib.import_module("._binding", __name__)
-        return getattr(binding, name)
-    if name in _TOKEN_EXPORTS:
-        tokens = importlib.import_module("._tokens", __name__)
-        return getattr(tokens, name)
+    for exports, module in ((_EXPORTS, "._binding"), (_TOKEN_EXPORTS, "._tokens")):
+        if name in exports:
+            value = getattr(importlib.import_module(module, __name__), name)
+            globals()[name] = value  # later uses find it without this call
+            return value
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -7,14 +7,18 @@ tensors' device, made current around the call where it is not.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 from typing import Optional
 
 import torch
 
-from ._binding import (_need, _P, _ptr, _stream, _sz, _vp, RI_OK, RIError, STATUS_CODES,
+from ._binding import (_need, _P, _ptr, _sz, _vp, RI_OK, RIError, STATUS_CODES,
                        alloc_workspace, check, lib)
+
+# the current device and a device's current stream without torch.cuda's
+# wrappers: a decode step makes these calls once each, and they are cheap
+_current_device = torch._C._cuda_getDevice
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 BF16, FP16, FP32 = 0, 1, 2
 _DTYPES = {torch.bfloat16: BF16, torch.float16: FP16, torch.float32: FP32}
@@ -70,16 +74,27 @@ lib.ri_token_evict.restype = ctypes.c_int
 lib.ri_token_evict.argtypes = [_P(CTokenCache), _i32, _i32, _i32, _P(CTokenCache), _vp, _sz, _vp]
 
 
-_NOTHING = contextlib.nullcontext()
-
-
-def _on(dev: torch.device):
-    """The device of a call's tensors made current, where it is not already."""
+def _run(dev: torch.device, fn, where: str, *args) -> None:
+    """fn(*args, stream) on torch's current stream of the tensors' device, which
+    is made current around the call where it is not."""
     if dev.type != "cuda":
         raise ValueError("the token cache's calls need CUDA tensors")
-    if dev.index is None or dev.index == torch.cuda.current_device():
-        return _NOTHING
-    return torch.cuda.device(dev)
+    i = dev.index
+    if i == _current_device():
+        rc = fn(*args, _raw_stream(i))
+    else:
+        with torch.cuda.device(i):
+            rc = fn(*args, _raw_stream(i))
+    if rc != RI_OK:
+        raise RIError(rc, where)
+
+
+def _dense(t, name: str, dtype: torch.dtype, shape: tuple, dev) -> int:
+    """The address of a contiguous tensor of this dtype, shape and device."""
+    if type(t) is not torch.Tensor or t.dtype != dtype or t.shape != shape or \
+            t.device != dev or not t.is_contiguous():
+        _need(t, name, dtype, shape, dev)
+    return t.data_ptr()
 
 
 class RotaryTable:
@@ -152,7 +167,7 @@ def _positions(pos: torch.Tensor, B: int, T: int, dev) -> int:
 
 def _no_overlap(out: torch.Tensor, name: str) -> None:
     """A written tensor addresses every element once (no stride-0 views)."""
-    if any(s == 0 and n > 1 for s, n in zip(out.stride(), out.shape)):
+    if 0 in out.stride() and any(s == 0 and n > 1 for s, n in zip(out.stride(), out.shape)):
         raise ValueError(f"{name} must not repeat elements (a stride of 0)")
 
 
@@ -168,22 +183,20 @@ def rotary(x: torch.Tensor, positions: torch.Tensor, table: RotaryTable,
         raise ValueError("x must be a tensor [batch][tokens][heads][head_dim]")
     if x.dtype not in _DTYPES:
         raise TypeError(f"x must be bfloat16, float16 or float32, got {x.dtype}")
-    dev = x.device
+    dev, shape, dtype = x.device, x.shape, x.dtype
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=dev)
-    cx = _heads(x, "x", x.dtype, x.shape, dev)
-    co = _heads(out, "out", x.dtype, x.shape, dev)
+        out = torch.empty(shape, dtype=dtype, device=dev)
+    cx = _heads(x, "x", dtype, shape, dev)
+    co = _heads(out, "out", dtype, shape, dev)
     _no_overlap(out, "out")
-    B, T, H, d = x.shape
+    B, T, H, d = shape
     sb = _positions(positions, B, T, dev)
     if table.turns.device != dev:
         raise ValueError(f"table must be on {dev}, got {table.turns.device}")
     if x.numel() == 0:
         return out
-    with _on(dev):
-        check(lib.ri_rotary(B, T, H, d, _DTYPES[x.dtype], ctypes.byref(cx), positions.data_ptr(),
-                            sb, table._ref, ctypes.byref(co), 1 if inverse else 0, _stream(dev)),
-              "ri_rotary")
+    _run(dev, lib.ri_rotary, "ri_rotary", B, T, H, d, _DTYPES[x.dtype], ctypes.byref(cx),
+         positions.data_ptr(), sb, table._ref, ctypes.byref(co), 1 if inverse else 0)
     return out
 
 
@@ -251,19 +264,16 @@ def token_append(cache: TokenCache, k: torch.Tensor, v: torch.Tensor, positions:
         cq = ctypes.byref(_heads(q, "q", torch.bfloat16, shape, dev))
         if q_out is None:
             q_out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
-        _need(q_out, "q_out", torch.bfloat16, shape, dev)
+        _dense(q_out, "q_out", torch.bfloat16, shape, dev)
     elif q_out is not None:
         raise ValueError("q_out needs q")
     if lens_out is None:
         lens_out = cache.lens
     else:
-        _need(lens_out, "lens_out", torch.int32, (B, H), dev)
-    with _on(dev):
-        check(lib.ri_token_append(cache._ref, T, ctypes.byref(ck), ctypes.byref(cv),
-                                  positions.data_ptr(), sb,
-                                  None if table is None else table._ref, cq, _ptr(q_out),
-                                  lens_out.data_ptr(), cache.status.data_ptr(), _stream(dev)),
-              "ri_token_append")
+        _dense(lens_out, "lens_out", torch.int32, (B, H), dev)
+    _run(dev, lib.ri_token_append, "ri_token_append", cache._ref, T, ctypes.byref(ck),
+         ctypes.byref(cv), positions.data_ptr(), sb, None if table is None else table._ref, cq,
+         _ptr(q_out), lens_out.data_ptr(), cache.status.data_ptr())
     return q_out
 
 
@@ -285,7 +295,7 @@ def token_attend(q: torch.Tensor, cache: TokenCache, prefix: Optional[tuple] = N
     Returns (out bf16 [B][H_q][128], lse fp32 [B][H_q])."""
     B, H, d, dev = cache.batch, cache.num_kv_heads, cache.head_dim, cache.device
     shape = (B, H * cache.group_size, d)
-    _need(q, "q", torch.bfloat16, shape, dev)
+    q_ptr = _dense(q, "q", torch.bfloat16, shape, dev)
     cp, P = None, 0
     if prefix is not None:
         K, V = prefix
@@ -310,20 +320,17 @@ def token_attend(q: torch.Tensor, cache: TokenCache, prefix: Optional[tuple] = N
     if out is None:
         out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
     else:
-        _need(out, "out", torch.bfloat16, shape, dev)
+        _dense(out, "out", torch.bfloat16, shape, dev)
     if lse is None:
         lse = torch.empty(shape[:2], dtype=torch.float32, device=dev)
     else:
-        _need(lse, "lse", torch.float32, shape[:2], dev)
+        _dense(lse, "lse", torch.float32, shape[:2], dev)
     if workspace is None:
         workspace = alloc_workspace(token_attend_workspace_bytes(cache, P), dev)
     elif workspace.device != dev:
         raise ValueError(f"workspace must be on {dev}, got {workspace.device}")
-    with _on(dev):
-        check(lib.ri_token_attend(cache._ref, q.data_ptr(), cp, out.data_ptr(), lse.data_ptr(),
-                                  1 if add_weight else 0, workspace.data_ptr(),
-                                  workspace.numel(), _stream(dev)),
-              "ri_token_attend")
+    _run(dev, lib.ri_token_attend, "ri_token_attend", cache._ref, q_ptr, cp, out.data_ptr(),
+         lse.data_ptr(), 1 if add_weight else 0, workspace.data_ptr(), workspace.numel())
     return out, lse
 
 
@@ -350,8 +357,6 @@ def token_evict(cache: TokenCache, budget: int, keep_first: int = 4, keep_recent
         workspace = alloc_workspace(token_evict_workspace_bytes(cache, budget), dev)
     elif workspace.device != dev:
         raise ValueError(f"workspace must be on {dev}, got {workspace.device}")
-    with _on(dev):
-        check(lib.ri_token_evict(cache._ref, budget, keep_first, keep_recent, out._ref,
-                                 workspace.data_ptr(), workspace.numel(), _stream(dev)),
-              "ri_token_evict")
+    _run(dev, lib.ri_token_evict, "ri_token_evict", cache._ref, budget, keep_first, keep_recent,
+         out._ref, workspace.data_ptr(), workspace.numel())
     return out

@@ -7,6 +7,7 @@
 #include <stdio.h>
 #include <string.h>
 
+#include <atomic>
 #include <cmath>
 #include <mutex>
 
@@ -27,11 +28,17 @@ void set_error(const char* fmt, ...) {
 }
 
 int num_sms() {
+  constexpr int kMany = 64;
+  static std::atomic<int> known[kMany];  // per device, 0: not asked yet
   int dev = 0, n = 148;
   if (cudaGetDevice(&dev) == cudaSuccess) {
+    if (dev >= 0 && dev < kMany && known[dev].load(std::memory_order_relaxed) > 0)
+      return known[dev].load(std::memory_order_relaxed);
     int v = 0;
-    if (cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess && v > 0)
+    if (cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess && v > 0) {
       n = v;
+      if (dev >= 0 && dev < kMany) known[dev].store(v, std::memory_order_relaxed);
+    }
   }
   return n;
 }

@@ -68,142 +68,165 @@ struct alignas(VEC * sizeof(T)) Pack {
   T v[VEC];
 };
 
-template <typename T, int VEC>
-__device__ __forceinline__ Pack<T, VEC> load(const T* p) {
-  return *reinterpret_cast<const Pack<T, VEC>*>(p);
-}
-template <typename T, int VEC>
-__device__ __forceinline__ void store(T* p, const Pack<T, VEC>& v) {
-  *reinterpret_cast<Pack<T, VEC>*>(p) = v;
-}
-
 // A head's accesses ("items"): rotated ones first, then copies of the rest.
-// Half layout: item i turns elements [i VEC, +VEC) with those n further on.
-// Interleaved: item i turns the pairs inside elements [i W, +W), W = VEC (at
-// least a pair).
-template <int VEC>
-struct Items {
-  int n, turned, count, inter;  // pairs, rotated items, all items, layout
-  __host__ __device__ Items(int rotary_dim, int interleaved, int d) {
-    n = rotary_dim / 2;
-    inter = interleaved;
-    const int w = VEC > 1 ? VEC : 2;
-    turned = interleaved ? rotary_dim / w : n / VEC;
-    count = turned + (d - rotary_dim) / VEC;
+//  half layout  item i turns elements [i VEC, +VEC) with those n further on;
+//  interleaved  item i turns the pairs inside elements [i W, +W), W = VEC (at
+//               least a pair).
+// VEC is 16 bytes' worth of elements where every row and both halves start on
+// 16 bytes, else 1.
+template <typename T, int VEC, bool INTER>
+struct Item {
+  static constexpr int W = VEC > 1 ? VEC : 2;
+  static constexpr int kPairs = INTER ? W / 2 : VEC;
+  static constexpr int kElems = INTER ? W : 2 * VEC;
+  int n;       // pairs of a head
+  int at;      // first element
+  bool turns;
+
+  static __host__ __device__ int turned(int rotary_dim) {
+    return INTER ? rotary_dim / W : rotary_dim / 2 / VEC;
+  }
+  static __host__ __device__ int count(int rotary_dim, int d) {
+    return turned(rotary_dim) + (d - rotary_dim) / VEC;
+  }
+  __device__ __forceinline__ Item(int item, int rotary_dim) : n(rotary_dim / 2) {
+    const int k = turned(rotary_dim);
+    turns = item < k;
+    at = turns ? item * (INTER ? W : VEC) : rotary_dim + (item - k) * VEC;
+  }
+  __device__ __forceinline__ void angles(const ri_rope& rope, int pos, float sign,
+                                         float (&c)[kPairs], float (&s)[kPairs]) const {
+    if (!turns) return;
+    const unsigned long long* turns_of =
+        reinterpret_cast<const unsigned long long*>(rope.turns) + (INTER ? at / 2 : at);
+#pragma unroll
+    for (int i = 0; i < kPairs; ++i) {
+      turn_angle(__ldg(turns_of + i), pos, rope.magnitude, &c[i], &s[i]);
+      s[i] *= sign;
+    }
+  }
+  __device__ __forceinline__ void load(const T* row, T (&e)[kElems]) const {
+    take<VEC>(row + at, e, 0);
+    if (turns) {
+      if (!INTER) take<VEC>(row + at + n, e, VEC);
+      else if (VEC == 1) take<1>(row + at + 1, e, 1);
+    }
+  }
+  __device__ __forceinline__ void store(T* row, const T (&e)[kElems]) const {
+    put<VEC>(row + at, e, 0);
+    if (turns) {
+      if (!INTER) put<VEC>(row + at + n, e, VEC);
+      else if (VEC == 1) put<1>(row + at + 1, e, 1);
+    }
+  }
+  __device__ __forceinline__ void turn(T (&e)[kElems], const float (&c)[kPairs],
+                                       const float (&s)[kPairs]) const {
+    if (!turns) return;
+#pragma unroll
+    for (int i = 0; i < kPairs; ++i) {
+      const int ia = INTER ? 2 * i : i, ib = INTER ? 2 * i + 1 : i + VEC;
+      const float a = to_f(e[ia]), b = to_f(e[ib]);
+      e[ia] = from_f<T>(a * c[i] - b * s[i]);
+      e[ib] = from_f<T>(b * c[i] + a * s[i]);
+    }
+  }
+
+ private:
+  template <int N>
+  static __device__ __forceinline__ void take(const T* p, T (&e)[kElems], int to) {
+    const Pack<T, N> v = *reinterpret_cast<const Pack<T, N>*>(p);
+#pragma unroll
+    for (int i = 0; i < N; ++i) e[to + i] = v.v[i];
+  }
+  template <int N>
+  static __device__ __forceinline__ void put(T* p, const T (&e)[kElems], int from) {
+    Pack<T, N> v;
+#pragma unroll
+    for (int i = 0; i < N; ++i) v.v[i] = e[from + i];
+    *reinterpret_cast<Pack<T, N>*>(p) = v;
   }
 };
 
-template <int VEC>
-__device__ __forceinline__ void item_angles(const ri_rope& rope, const Items<VEC>& it, int item,
-                                            int pos, float sign, float (&c)[VEC], float (&s)[VEC]) {
-  if (item >= it.turned) return;
-  constexpr int kInter = VEC > 1 ? VEC / 2 : 1;
-  if (it.inter) {
-#pragma unroll
-    for (int i = 0; i < kInter; ++i) {
-      turn_angle(__ldg(reinterpret_cast<const unsigned long long*>(rope.turns) + item * kInter + i),
-                 pos, rope.magnitude, &c[i], &s[i]);
-      s[i] *= sign;
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) {
-      turn_angle(__ldg(reinterpret_cast<const unsigned long long*>(rope.turns) + item * VEC + i),
-                 pos, rope.magnitude, &c[i], &s[i]);
-      s[i] *= sign;
-    }
-  }
+// A block's 256 threads: `lanes` items of a row, fastest, so that a row is one
+// contiguous access; then `row_slots` rows; then tokens.  A thread computes
+// its item's angles once and uses them for every row of its token and group
+// that falls to its slot, kBatch rows in flight.
+struct Shape {
+  int lanes, row_slots;  // powers of two
+  int items;
+  int group_rows;        // rows (heads) of a group, blockIdx.y counts the groups
+};
+constexpr int kBatch = 4;
+constexpr int kMaxGridDim = 65535;  // of y and z
+
+// Rows of a token and how many of them a group takes: the largest group whose
+// grid still gives every SM four blocks.
+Shape shape_of(int items, int tokens, int batch, int units, int rows_per_unit) {
+  Shape s;
+  s.items = items;
+  s.lanes = 1;
+  while (s.lanes < items && s.lanes < kThreads) s.lanes *= 2;
+  int token_slots = kThreads / s.lanes;
+  while (token_slots > 1 && token_slots / 2 >= tokens) token_slots /= 2;
+  s.row_slots = kThreads / s.lanes / token_slots;
+  const long long blocks = (long long)batch * ((tokens + token_slots - 1) / token_slots);
+  int per = units;  // a group: units with their rows
+  while (per > 1 && blocks * ((units + per - 1) / per) < 4ll * num_sms()) per = (per + 1) / 2;
+  while ((units + per - 1) / per > kMaxGridDim) per *= 2;
+  s.group_rows = per * rows_per_unit;
+  return s;
 }
 
-// One item of one head: src -> dst (which may be the same row).
-template <typename T, int VEC>
-__device__ __forceinline__ void turn_item(const T* src, T* dst, const Items<VEC>& it, int item,
-                                          const float (&c)[VEC], const float (&s)[VEC]) {
-  if (item >= it.turned) {
-    const int at = 2 * it.n + (item - it.turned) * VEC;
-    store<T, VEC>(dst + at, load<T, VEC>(src + at));
-    return;
-  }
-  if (it.inter) {
-    constexpr int W = VEC > 1 ? VEC : 2;
-    const int at = item * W;
-    T x[W];
-    if constexpr (VEC > 1) {
-      const Pack<T, VEC> p = load<T, VEC>(src + at);
-#pragma unroll
-      for (int i = 0; i < W; ++i) x[i] = p.v[i];
-    } else {
-      x[0] = src[at];
-      x[1] = src[at + 1];
-    }
-#pragma unroll
-    for (int i = 0; i < W / 2; ++i) {
-      const float a = to_f(x[2 * i]), b = to_f(x[2 * i + 1]);
-      x[2 * i] = from_f<T>(a * c[i] - b * s[i]);
-      x[2 * i + 1] = from_f<T>(b * c[i] + a * s[i]);
-    }
-    if constexpr (VEC > 1) {
-      Pack<T, VEC> p;
-#pragma unroll
-      for (int i = 0; i < W; ++i) p.v[i] = x[i];
-      store<T, VEC>(dst + at, p);
-    } else {
-      dst[at] = x[0];
-      dst[at + 1] = x[1];
-    }
-    return;
-  }
-  const int at = item * VEC;
-  Pack<T, VEC> p = load<T, VEC>(src + at), r = load<T, VEC>(src + at + it.n);
-#pragma unroll
-  for (int i = 0; i < VEC; ++i) {
-    const float a = to_f(p.v[i]), b = to_f(r.v[i]);
-    p.v[i] = from_f<T>(a * c[i] - b * s[i]);
-    r.v[i] = from_f<T>(b * c[i] + a * s[i]);
-  }
-  store<T, VEC>(dst + at, p);
-  store<T, VEC>(dst + at + it.n, r);
+dim3 grid_of(const Shape& s, int tokens, int batch, int rows) {
+  const int token_slots = kThreads / s.lanes / s.row_slots;
+  return dim3((unsigned)((tokens + token_slots - 1) / token_slots),
+              (unsigned)((rows + s.group_rows - 1) / s.group_rows), (unsigned)batch);
 }
 
-// One thread per (token, group of `per` heads, item), items fastest so that
-// neighbouring threads share rows; the angles are computed once and used for
-// all heads of the group.
-template <typename T, int VEC>
-__global__ void __launch_bounds__(kThreads)
-    rotary_kernel(RotaryArgs a, int per, int groups, int copy_rest) {
-  const Items<VEC> it(a.rope.rotary_dim, a.rope.interleaved, a.d);
-  const int items = copy_rest ? it.count : it.turned;
-  const long long total = (long long)a.B * a.T * groups * items;
-  for (long long i = (long long)blockIdx.x * kThreads + threadIdx.x; i < total;
-       i += (long long)gridDim.x * kThreads) {
-    const int item = (int)(i % items);
-    long long r = i / items;
-    const int g = (int)(r % groups);
-    r /= groups;
-    const int t = (int)(r % a.T);
-    const int b = (int)(r / a.T);
-    float c[VEC], s[VEC];
-    item_angles<VEC>(a.rope, it, item, a.pos[b * a.pos_stride + t], a.inverse ? -1.f : 1.f, c, s);
+template <typename T, int VEC, bool INTER>
+__global__ void __launch_bounds__(kThreads) rotary_kernel(const RotaryArgs a, const Shape sh) {
+  using I = Item<T, VEC, INTER>;
+  const int lane = threadIdx.x & (sh.lanes - 1), slot = threadIdx.x / sh.lanes;
+  const int token_slots = kThreads / sh.lanes / sh.row_slots;
+  const int t = blockIdx.x * token_slots + slot / sh.row_slots;
+  if (t >= a.T) return;
+  const int r1 = min(a.heads, (int)(blockIdx.y + 1) * sh.group_rows);
+  for (int b = blockIdx.z; b < a.B; b += gridDim.z) {
+    const int pos = a.pos[b * a.pos_stride + t];
     const T* x = static_cast<const T*>(a.x.data) + b * a.x.stride_b + t * a.x.stride_t;
     T* y = static_cast<T*>(a.out.data) + b * a.out.stride_b + t * a.out.stride_t;
-    const int h1 = min(a.heads, (g + 1) * per);
-#pragma unroll 4
-    for (int h = g * per; h < h1; ++h)
-      turn_item<T, VEC>(x + h * a.x.stride_h, y + h * a.out.stride_h, it, item, c, s);
+    for (int i = lane; i < sh.items; i += sh.lanes) {
+      const I item(i, a.rope.rotary_dim);
+      float c[I::kPairs], s[I::kPairs];
+      item.angles(a.rope, pos, a.inverse ? -1.f : 1.f, c, s);
+      for (int r = blockIdx.y * sh.group_rows + (slot & (sh.row_slots - 1)); r < r1;
+           r += kBatch * sh.row_slots) {
+        T e[kBatch][I::kElems];
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j)
+          if (r + j * sh.row_slots < r1)
+            item.load(x + (r + j * sh.row_slots) * a.x.stride_h, e[j]);
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j)
+          if (r + j * sh.row_slots < r1) {
+            item.turn(e[j], c, s);
+            item.store(y + (r + j * sh.row_slots) * a.out.stride_h, e[j]);
+          }
+      }
+    }
   }
 }
 
-template <typename T, int VEC>
+template <typename T, int VEC, bool INTER>
 cudaError_t rotary_typed(const RotaryArgs& a, cudaStream_t s) {
-  const Items<VEC> it(a.rope.rotary_dim, a.rope.interleaved, a.d);
-  const bool in_place = a.x.data == a.out.data;
-  const int items = in_place ? it.turned : it.count;
-  const int per = a.heads < 8 ? a.heads : 8;
-  const int groups = (a.heads + per - 1) / per;
-  const long long total = (long long)a.B * a.T * groups * items;
-  long long blocks = (total + kThreads - 1) / kThreads;
-  if (blocks > (1 << 30)) blocks = 1 << 30;
-  rotary_kernel<T, VEC><<<(unsigned)blocks, kThreads, 0, s>>>(a, per, groups, !in_place);
+  using I = Item<T, VEC, INTER>;
+  const int n = a.rope.rotary_dim;
+  // in place the rest of the head stays where it is
+  const int items = a.x.data == a.out.data ? I::turned(n) : I::count(n, a.d);
+  const Shape sh = shape_of(items, a.T, a.B, a.heads, 1);
+  dim3 grid = grid_of(sh, a.T, a.B, a.heads);
+  if (grid.z > kMaxGridDim) grid.z = kMaxGridDim;
+  rotary_kernel<T, VEC, INTER><<<grid, kThreads, 0, s>>>(a, sh);
   return cudaGetLastError();
 }
 
@@ -215,74 +238,96 @@ bool vec_ok(const ri_heads& x, int size) {
 template <typename T>
 cudaError_t rotary_of(const RotaryArgs& a, cudaStream_t s) {
   constexpr int V = 16 / (int)sizeof(T);
-  const int run = a.rope.interleaved ? a.rope.rotary_dim : a.rope.rotary_dim / 2;
+  const bool inter = a.rope.interleaved;
+  const int run = inter ? a.rope.rotary_dim : a.rope.rotary_dim / 2;
   // whole 16-byte accesses where every row and both halves start on one
-  if (run % V == 0 && a.d % V == 0 && a.rope.rotary_dim % V == 0 && vec_ok(a.x, sizeof(T)) &&
-      vec_ok(a.out, sizeof(T)))
-    return rotary_typed<T, V>(a, s);
-  return rotary_typed<T, 1>(a, s);
+  const bool vec = run % V == 0 && a.d % V == 0 && a.rope.rotary_dim % V == 0 &&
+                   vec_ok(a.x, sizeof(T)) && vec_ok(a.out, sizeof(T));
+  if (vec) return inter ? rotary_typed<T, V, true>(a, s) : rotary_typed<T, V, false>(a, s);
+  return inter ? rotary_typed<T, 1, true>(a, s) : rotary_typed<T, 1, false>(a, s);
 }
 
 // ------------------------------------------------------------------- append
-// One warp per (sequence, token, KV head): its G query heads, its key and its
-// value.  The rows of a warp are dealt to groups of lanes, one item per lane.
-template <int VEC>
-__global__ void __launch_bounds__(kThreads) append_kernel(AppendTokensArgs a, int advance) {
+// The rows of a token are dealt by KV head: its G query heads, its key, its
+// value.  The value's row takes the same items, copied.
+template <int VEC, bool INTER>
+__global__ void __launch_bounds__(kThreads)
+    append_kernel(const AppendTokensArgs a, const Shape sh, int advance) {
   using T = __nv_bfloat16;
-  const int lane = threadIdx.x & 31;
-  const long long w = ((long long)blockIdx.x * kThreads + threadIdx.x) >> 5;
-  const int H = a.c.num_kv_heads, G = a.c.group_size;
-  if (w >= (long long)a.c.batch * a.T * H) return;
-  const int h = (int)(w % H);
-  const int t = (int)(w / H % a.T);
-  const int b = (int)(w / H / a.T);
-  const long long unit = (long long)b * H + h;
-  const int cap = a.c.capacity;
-  int len = a.c.lens[unit];
-  if (len < 0 || len > cap) {
-    if (lane == 0 && t == 0) record_status(a.status, RI_ERR_INVALID_ARG);
-    len = len < 0 ? 0 : cap;
-  }
-  const bool room = len + (long long)a.T <= cap;
-  if (!room && lane == 0 && t == 0) record_status(a.status, RI_ERR_CAPACITY);
-  __syncwarp();  // every lane has the length before lane 0 may replace it
-  const int pos = a.pos[b * a.pos_stride + t];
+  using I = Item<T, VEC, INTER>;
+  const int lane = threadIdx.x & (sh.lanes - 1), slot = threadIdx.x / sh.lanes;
+  const int token_slots = kThreads / sh.lanes / sh.row_slots;
+  const int t = blockIdx.x * token_slots + slot / sh.row_slots;
+  const int H = a.c.num_kv_heads, G = a.q.data ? a.c.group_size : 0, cap = a.c.capacity;
+  const int per = G + 2;  // rows of a KV head
+  const int r0 = blockIdx.y * sh.group_rows, r1 = min(H * per, r0 + sh.group_rows);
   const int n = a.rope.turns ? a.rope.rotary_dim : 0;
-  const Items<VEC> it(n, a.rope.interleaved, kHeadDim);
-  const long long row = unit * cap + len + t;
-  const int q_rows = a.q.data ? G : 0;
-  const int rows = q_rows + (room ? 1 : 0);
-  // lanes of a row: the items' count rounded up to a power of two, at most 32
-  int lpr = 1;
-  while (lpr < it.count && lpr < 32) lpr <<= 1;
-  const int sub = lane / lpr, subs = 32 / lpr;
-  for (int item = lane % lpr; item < it.count; item += lpr) {
-    float c[VEC], s[VEC];
-    item_angles<VEC>(a.rope, it, item, pos, 1.f, c, s);
-    for (int r = sub; r < rows; r += subs) {
-      const T* src;
-      T* dst;
-      if (r < q_rows) {
-        src = static_cast<const T*>(a.q.data) + b * a.q.stride_b + t * a.q.stride_t +
-              (long long)(h * G + r) * a.q.stride_h;
-        dst = static_cast<T*>(a.q_out) + (((long long)b * a.T + t) * H * G + h * G + r) * kHeadDim;
-      } else {
-        src = static_cast<const T*>(a.k.data) + b * a.k.stride_b + t * a.k.stride_t +
-              h * a.k.stride_h;
-        dst = static_cast<T*>(a.c.K) + row * kHeadDim;
+  for (int b = blockIdx.z; b < a.c.batch; b += gridDim.z) {
+    if (t < a.T) {
+      const int pos = a.pos[b * a.pos_stride + t];
+      for (int i = lane; i < sh.items; i += sh.lanes) {
+        const I item(i, n);
+        float c[I::kPairs], s[I::kPairs];
+        item.angles(a.rope, pos, 1.f, c, s);
+        for (int r = r0 + (slot & (sh.row_slots - 1)); r < r1; r += kBatch * sh.row_slots) {
+          T e[kBatch][I::kElems];
+          T* dst[kBatch];
+#pragma unroll
+          for (int j = 0; j < kBatch; ++j) {
+            const int row = r + j * sh.row_slots;
+            dst[j] = nullptr;
+            if (row >= r1) continue;
+            const int h = row / per, k = row - h * per;
+            const T* src;
+            if (k < G) {
+              src = static_cast<const T*>(a.q.data) + b * a.q.stride_b + t * a.q.stride_t +
+                    (long long)(h * G + k) * a.q.stride_h;
+              dst[j] = static_cast<T*>(a.q_out) +
+                       (((long long)b * a.T + t) * H * G + h * G + k) * kHeadDim;
+            } else {
+              const long long unit = (long long)b * H + h;
+              const int len = a.c.lens[unit];
+              const bool live = len >= 0 && len <= cap;
+              const int at = live ? len : len < 0 ? 0 : cap;
+              const bool room = at + (long long)a.T <= cap;
+              if (k == G && i == 0 && t == 0) {
+                if (!live) record_status(a.status, RI_ERR_INVALID_ARG);
+                if (!room) record_status(a.status, RI_ERR_CAPACITY);
+              }
+              if (!room) continue;
+              const ri_heads& x = k == G ? a.k : a.v;
+              src = static_cast<const T*>(x.data) + b * x.stride_b + t * x.stride_t +
+                    h * x.stride_h;
+              const long long to = unit * cap + at + t;
+              dst[j] = static_cast<T*>(k == G ? a.c.K : a.c.V) + to * kHeadDim;
+              if (k == G && i == 0) {
+                a.c.pos[to] = pos;
+                a.c.weight[to] = 0.f;
+              }
+            }
+            item.load(src, e[j]);
+          }
+#pragma unroll
+          for (int j = 0; j < kBatch; ++j)
+            if (dst[j]) {
+              const int row = r + j * sh.row_slots;
+              if (row % per != per - 1) item.turn(e[j], c, s);  // not the value
+              item.store(dst[j], e[j]);
+            }
+        }
       }
-      turn_item<T, VEC>(src, dst, it, item, c, s);
+    }
+    if (advance) {
+      // a unit's key and value lie in one block: with one token (or lengths
+      // that go elsewhere) this block is the last to need its length
+      __syncthreads();
+      for (int h = r0 / per + threadIdx.x; h < r1 / per; h += kThreads)
+        if (blockIdx.x == 0) {
+          const int u = b * H + h, len = min(max(a.c.lens[u], 0), cap);
+          a.lens_out[u] = len + (long long)a.T <= cap ? len + a.T : len;
+        }
     }
   }
-  if (room) {
-    const T* src = static_cast<const T*>(a.v.data) + b * a.v.stride_b + t * a.v.stride_t +
-                   h * a.v.stride_h;
-    T* dst = static_cast<T*>(a.c.V) + row * kHeadDim;
-    if (lane < 16) store<T, 8>(dst + lane * 8, load<T, 8>(src + lane * 8));
-    if (lane == 16) a.c.pos[row] = pos;
-    if (lane == 17) a.c.weight[row] = 0.f;
-  }
-  if (advance && t == 0 && lane == 0) a.lens_out[unit] = room ? len + a.T : len;
 }
 
 // Advances the lengths in place once every token of append_kernel is stored.
@@ -291,6 +336,25 @@ __global__ void advance_kernel(int32_t* lens, int units, int cap, int T) {
   if (u >= units) return;
   const int len = min(max(lens[u], 0), cap);
   lens[u] = len + (long long)T <= cap ? len + T : len;
+}
+
+template <int VEC, bool INTER>
+cudaError_t append_typed(const AppendTokensArgs& a, cudaStream_t s) {
+  using I = Item<__nv_bfloat16, VEC, INTER>;
+  const int n = a.rope.turns ? a.rope.rotary_dim : 0;
+  const int H = a.c.num_kv_heads, per = (a.q.data ? a.c.group_size : 0) + 2;
+  const Shape sh = shape_of(I::count(n, kHeadDim), a.T, a.c.batch, H, per);
+  dim3 grid = grid_of(sh, a.T, a.c.batch, H * per);
+  if (grid.z > kMaxGridDim) grid.z = kMaxGridDim;
+  // several tokens in place: other blocks may still read a length, so a second
+  // launch advances them
+  const bool later = a.lens_out == a.c.lens && a.T > 1;
+  append_kernel<VEC, INTER><<<grid, kThreads, 0, s>>>(a, sh, !later);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess || !later) return e;
+  const int units = a.c.batch * H;
+  advance_kernel<<<(units + 255) / 256, 256, 0, s>>>(a.c.lens, units, a.c.capacity, a.T);
+  return cudaGetLastError();
 }
 
 }  // namespace
@@ -304,22 +368,11 @@ cudaError_t launch_rotary(const RotaryArgs& a, int dtype, cudaStream_t s) {
 }
 
 cudaError_t launch_token_append(const AppendTokensArgs& a, cudaStream_t s) {
-  const long long warps = (long long)a.c.batch * a.T * a.c.num_kv_heads;
-  const unsigned blocks = (unsigned)((warps * 32 + kThreads - 1) / kThreads);
-  // one token per unit: the warp that reads a length is the one that replaces
-  // it; several: other warps may still read it, so a second launch advances it
-  const bool later = a.lens_out == a.c.lens && a.T > 1;
   const int n = a.rope.turns ? a.rope.rotary_dim : 0;
-  const int run = a.rope.interleaved ? n : n / 2;
-  if (run % 8 == 0 && n % 8 == 0)
-    append_kernel<8><<<blocks, kThreads, 0, s>>>(a, !later);
-  else
-    append_kernel<1><<<blocks, kThreads, 0, s>>>(a, !later);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess || !later) return e;
-  const int units = a.c.batch * a.c.num_kv_heads;
-  advance_kernel<<<(units + 255) / 256, 256, 0, s>>>(a.c.lens, units, a.c.capacity, a.T);
-  return cudaGetLastError();
+  const bool inter = n > 0 && a.rope.interleaved;
+  const bool vec = (inter ? n : n / 2) % 8 == 0 && n % 8 == 0;
+  if (vec) return inter ? append_typed<8, true>(a, s) : append_typed<8, false>(a, s);
+  return inter ? append_typed<1, true>(a, s) : append_typed<1, false>(a, s);
 }
 
 }  // namespace ri
