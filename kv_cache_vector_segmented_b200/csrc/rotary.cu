@@ -5,13 +5,13 @@
 // A position far out (p * f of 10^6 radians) loses all its fraction in fp32,
 // so the table holds f / 2 pi as a 64-bit fraction of a turn: the product
 // with the position, modulo 2^64, IS the angle's fraction of a turn, exact to
-// 2^-64 * p, in two integer multiplications.  Its top 32 bits as a signed
-// number of half turns go to sincospif.  The rotation runs in fp32 and is
+// 2^-64 * p, in two integer multiplications.  The rotation runs in fp32 and is
 // rounded once to the tensor's type.
 //
-// What bounds it: memory (each element read and written once); the angle of a
-// pair is computed once per thread and used for every head the thread takes.
+// What bounds it: memory (each element read and written once).
 #include <cuda_fp16.h>
+
+#include <type_traits>
 
 #include "common.cuh"
 #include "internal.h"
@@ -21,16 +21,32 @@ namespace ri {
 namespace {
 
 constexpr int kThreads = 256;
+// blocks a grid has per SM: three fit at 64 KB of ring each, the fourth evens
+// out the end (128K tokens of 8 heads: 93 us against 99 us with three)
+constexpr int kBlocksPerSm = 4;
+constexpr int kBatch = 4;  // rows of copies a thread issues at a time, one batch ahead
 
+// Cosine and sine of pos * turns / 2^64 turns, times magnitude.  The fraction's
+// top two bits (after adding an eighth) are the quadrant, the rest an angle x
+// of at most pi / 4: sin x = x + x^3 p(x^2), cos x = 1 - x^2 / 2 + x^4 q(x^2)
+// with p, q interpolated at Chebyshev nodes (off by 8.1e-9 and 5.9e-10).
+// About 25 instructions; sincospif took about 185 and was the bound.
 __device__ __forceinline__ void turn_angle(unsigned long long turns, int pos, float magnitude,
                                            float* c, float* s) {
-  const unsigned long long t = static_cast<unsigned long long>(static_cast<long long>(pos)) * turns;
-  // [-2^31, 2^31) of 2^-31 half turns; the cut bits are 2^-32 of a turn
-  const float half_turns = static_cast<float>(static_cast<int>(t >> 32)) * 0x1p-31f;
-  float sv, cv;
-  sincospif(half_turns, &sv, &cv);
-  *c = cv * magnitude;
-  *s = sv * magnitude;
+  const uint32_t t = static_cast<uint32_t>(
+      (static_cast<unsigned long long>(static_cast<long long>(pos)) * turns) >> 32);
+  const uint32_t q = (t + 0x20000000u) >> 30;
+  const float x = static_cast<float>(static_cast<int>(t - (q << 30))) * 1.4629180792671596e-9f;
+  const float u = x * x;
+  const float sx = fmaf(
+      x * u, fmaf(u, fmaf(u, -0.00019587890710681677f, 0.008332747966051102f), -0.166666641831398f),
+      x);
+  const float cx = fmaf(
+      u * u, fmaf(u, fmaf(u, 2.454794230288826e-05f, -0.001388830249197781f), 0.0416666641831398f),
+      fmaf(u, -0.5f, 1.f));
+  const float sv = (q & 1) ? cx : sx, cv = (q & 1) ? sx : cx;
+  *s = __uint_as_float(__float_as_uint(sv * magnitude) ^ ((q & 2) << 30));
+  *c = __uint_as_float(__float_as_uint(cv * magnitude) ^ (((q + 1) & 2) << 30));
 }
 
 template <typename T>
@@ -62,171 +78,344 @@ __device__ __forceinline__ float from_f<float>(float v) {
   return v;
 }
 
-// VEC elements moved by one access (16 bytes, or one element).
-template <typename T, int VEC>
-struct alignas(VEC * sizeof(T)) Pack {
-  T v[VEC];
-};
+// ------------------------------------------------------- 16 bytes at a time
+// V = 16 / sizeof(T) elements of an access, as floats and back.
+template <typename T>
+__device__ __forceinline__ void unpack(const uint4& v, float (&f)[16 / sizeof(T)]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (sizeof(T) == 4) {
+      f[i] = __uint_as_float(w[i]);
+    } else if constexpr (std::is_same<T, __half>::value) {
+      const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+      f[2 * i] = x.x;
+      f[2 * i + 1] = x.y;
+    } else {
+      f[2 * i] = __uint_as_float(w[i] << 16);
+      f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+  }
+}
+template <typename T>
+__device__ __forceinline__ uint4 pack(const float (&f)[16 / sizeof(T)]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (sizeof(T) == 4) {
+      w[i] = __float_as_uint(f[i]);
+    } else if constexpr (std::is_same<T, __half>::value) {
+      const __half2 h = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t*>(&h);
+    } else {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
 
-// A head's accesses ("items"): rotated ones first, then copies of the rest.
-//  half layout  item i turns elements [i VEC, +VEC) with those n further on;
-//  interleaved  item i turns the pairs inside elements [i W, +W), W = VEC (at
-//               least a pair).
-// VEC is 16 bytes' worth of elements where every row and both halves start on
-// 16 bytes, else 1.
-template <typename T, int VEC, bool INTER>
-struct Item {
-  static constexpr int W = VEC > 1 ? VEC : 2;
-  static constexpr int kPairs = INTER ? W / 2 : VEC;
-  static constexpr int kElems = INTER ? W : 2 * VEC;
-  int n;       // pairs of a head
-  int at;      // first element
-  bool turns;
-
-  static __host__ __device__ int turned(int rotary_dim) {
-    return INTER ? rotary_dim / W : rotary_dim / 2 / VEC;
+// The rows (heads) of a token, in the order the kernels take them, and where
+// they come from and go to.  A row without a source is skipped.
+template <typename T>
+struct HeadRows {  // ri_rotary
+  static constexpr bool kAdvances = false;
+  RotaryArgs a;
+  __host__ __device__ int count() const { return a.heads; }
+  __device__ __forceinline__ bool turned(int) const { return true; }
+  __device__ __forceinline__ const T* from(int b, int t, int r) const {
+    return static_cast<const T*>(a.x.data) + b * a.x.stride_b + t * a.x.stride_t +
+           r * a.x.stride_h;
   }
-  static __host__ __device__ int count(int rotary_dim, int d) {
-    return turned(rotary_dim) + (d - rotary_dim) / VEC;
-  }
-  __device__ __forceinline__ Item(int item, int rotary_dim) : n(rotary_dim / 2) {
-    const int k = turned(rotary_dim);
-    turns = item < k;
-    at = turns ? item * (INTER ? W : VEC) : rotary_dim + (item - k) * VEC;
-  }
-  __device__ __forceinline__ void angles(const ri_rope& rope, int pos, float sign,
-                                         float (&c)[kPairs], float (&s)[kPairs]) const {
-    if (!turns) return;
-    const unsigned long long* turns_of =
-        reinterpret_cast<const unsigned long long*>(rope.turns) + (INTER ? at / 2 : at);
-#pragma unroll
-    for (int i = 0; i < kPairs; ++i) {
-      turn_angle(__ldg(turns_of + i), pos, rope.magnitude, &c[i], &s[i]);
-      s[i] *= sign;
-    }
-  }
-  __device__ __forceinline__ void load(const T* row, T (&e)[kElems]) const {
-    take<VEC>(row + at, e, 0);
-    if (turns) {
-      if (!INTER) take<VEC>(row + at + n, e, VEC);
-      else if (VEC == 1) take<1>(row + at + 1, e, 1);
-    }
-  }
-  __device__ __forceinline__ void store(T* row, const T (&e)[kElems]) const {
-    put<VEC>(row + at, e, 0);
-    if (turns) {
-      if (!INTER) put<VEC>(row + at + n, e, VEC);
-      else if (VEC == 1) put<1>(row + at + 1, e, 1);
-    }
-  }
-  __device__ __forceinline__ void turn(T (&e)[kElems], const float (&c)[kPairs],
-                                       const float (&s)[kPairs]) const {
-    if (!turns) return;
-#pragma unroll
-    for (int i = 0; i < kPairs; ++i) {
-      const int ia = INTER ? 2 * i : i, ib = INTER ? 2 * i + 1 : i + VEC;
-      const float a = to_f(e[ia]), b = to_f(e[ib]);
-      e[ia] = from_f<T>(a * c[i] - b * s[i]);
-      e[ib] = from_f<T>(b * c[i] + a * s[i]);
-    }
-  }
-
- private:
-  template <int N>
-  static __device__ __forceinline__ void take(const T* p, T (&e)[kElems], int to) {
-    const Pack<T, N> v = *reinterpret_cast<const Pack<T, N>*>(p);
-#pragma unroll
-    for (int i = 0; i < N; ++i) e[to + i] = v.v[i];
-  }
-  template <int N>
-  static __device__ __forceinline__ void put(T* p, const T (&e)[kElems], int from) {
-    Pack<T, N> v;
-#pragma unroll
-    for (int i = 0; i < N; ++i) v.v[i] = e[from + i];
-    *reinterpret_cast<Pack<T, N>*>(p) = v;
+  __device__ __forceinline__ T* to(int b, int t, int r, bool) const {
+    return static_cast<T*>(a.out.data) + b * a.out.stride_b + t * a.out.stride_t +
+           r * a.out.stride_h;
   }
 };
+struct StepRows {  // ri_token_append: the query heads, the keys, the values
+  using T = __nv_bfloat16;
+  static constexpr bool kAdvances = true;
+  AppendTokensArgs a;
+  int nq;  // query heads
+  // Who writes the lengths after the call: `apart` (into an array of their
+  // own), the thread that stores a unit's first key; in place with one token
+  // per sequence, that sequence's block at its end; else a second launch, as
+  // other blocks may still read them.
+  bool apart;
+  __host__ __device__ bool at_end() const { return !apart && a.T == 1; }
+  __device__ __forceinline__ void advance(int u) const {
+    const int cap = a.c.capacity, len = min(max(a.c.lens[u], 0), cap);
+    a.lens_out[u] = len + (long long)a.T <= cap ? len + a.T : len;
+  }
+  __host__ __device__ int count() const { return nq + 2 * a.c.num_kv_heads; }
+  __device__ __forceinline__ bool turned(int r) const { return r < nq + a.c.num_kv_heads; }
+  __device__ __forceinline__ const T* from(int b, int t, int r) const {
+    const bool q = r < nq, k = r < nq + a.c.num_kv_heads;
+    const ri_heads& x = q ? a.q : k ? a.k : a.v;
+    const int h = q ? r : k ? r - nq : r - nq - a.c.num_kv_heads;
+    return static_cast<const T*>(x.data) + b * x.stride_b + t * x.stride_t + h * x.stride_h;
+  }
+  // `first`: the thread that also writes the token's position and weight and
+  // reports a length out of range or a full head
+  __device__ __forceinline__ T* to(int b, int t, int r, bool first) const {
+    const int H = a.c.num_kv_heads, cap = a.c.capacity;
+    if (r < nq) return static_cast<T*>(a.q_out) + (((long long)b * a.T + t) * nq + r) * kHeadDim;
+    const bool k = r < nq + H;
+    const long long unit = (long long)b * H + (k ? r - nq : r - nq - H);
+    const int len = a.c.lens[unit];
+    const bool live = len >= 0 && len <= cap;
+    const int at = live ? len : len < 0 ? 0 : cap;
+    const bool room = at + (long long)a.T <= cap;
+    if (k && first && t == 0) {
+      if (!live) record_status(a.status, RI_ERR_INVALID_ARG);
+      if (!room) record_status(a.status, RI_ERR_CAPACITY);
+      if (apart) a.lens_out[unit] = room ? at + a.T : at;
+    }
+    if (!room) return nullptr;
+    const long long row = unit * cap + at + t;
+    if (k && first) {
+      a.c.pos[row] = a.pos[b * a.pos_stride + t];
+      a.c.weight[row] = 0.f;
+    }
+    return static_cast<T*>(k ? a.c.K : a.c.V) + row * kHeadDim;
+  }
+};
 
-// A block's 256 threads: `lanes` items of a row, fastest, so that a row is one
-// contiguous access; then `row_slots` rows; then tokens.  A thread computes
-// its item's angles once and uses them for every row of its token and group
-// that falls to its slot, kBatch rows in flight.
+// A block's 256 threads: `lanes` accesses ("items") of a row, fastest, so that
+// a row is one contiguous piece; then `row_slots` rows; then tokens.  Items:
+//  half layout  item i turns elements [i V, +V) with those n further on;
+//  interleaved  item i turns the pairs inside elements [i V, +V);
+//  the rest of the head is copied, V elements per item.
 struct Shape {
   int lanes, row_slots;  // powers of two
-  int items;
-  int group_rows;        // rows (heads) of a group, blockIdx.y counts the groups
+  int items, turned;     // items of a row, those that turn
+  int blocks;
 };
-constexpr int kBatch = 4;
-constexpr int kMaxGridDim = 65535;  // of y and z
 
-// Rows of a token and how many of them a group takes: the largest group whose
-// grid still gives every SM four blocks.
-Shape shape_of(int items, int tokens, int batch, int units, int rows_per_unit) {
+Shape shape_of(int turned, int items, long long tokens, int rows) {
   Shape s;
+  s.turned = turned;
   s.items = items;
   s.lanes = 1;
-  while (s.lanes < items && s.lanes < kThreads) s.lanes *= 2;
-  int token_slots = kThreads / s.lanes;
-  while (token_slots > 1 && token_slots / 2 >= tokens) token_slots /= 2;
-  s.row_slots = kThreads / s.lanes / token_slots;
-  const long long blocks = (long long)batch * ((tokens + token_slots - 1) / token_slots);
-  int per = units;  // a group: units with their rows
-  while (per > 1 && blocks * ((units + per - 1) / per) < 4ll * num_sms()) per = (per + 1) / 2;
-  while ((units + per - 1) / per > kMaxGridDim) per *= 2;
-  s.group_rows = per * rows_per_unit;
+  while (s.lanes < items) s.lanes *= 2;
+  const int slots = kThreads / s.lanes;
+  const int fill = kBlocksPerSm * num_sms();
+  // one row slot (angles serve all rows of a token) unless the grid would not
+  // fill the machine
+  s.row_slots = 1;
+  while (s.row_slots < slots && s.row_slots < rows && tokens / (slots / s.row_slots) < fill)
+    s.row_slots *= 2;
+  const int token_slots = slots / s.row_slots;
+  const long long tiles = (tokens + token_slots - 1) / token_slots;
+  s.blocks = (int)(tiles < fill ? tiles : fill);
   return s;
 }
 
-dim3 grid_of(const Shape& s, int tokens, int batch, int rows) {
-  const int token_slots = kThreads / s.lanes / s.row_slots;
-  return dim3((unsigned)((tokens + token_slots - 1) / token_slots),
-              (unsigned)((rows + s.group_rows - 1) / s.group_rows), (unsigned)batch);
-}
-
-template <typename T, int VEC, bool INTER>
-__global__ void __launch_bounds__(kThreads) rotary_kernel(const RotaryArgs a, const Shape sh) {
-  using I = Item<T, VEC, INTER>;
+// Every thread walks its tokens and their rows through a ring of its own in
+// shared memory, kBatch to 2 kBatch rows of asynchronous copies ahead: no
+// registers hold loads in flight and no barrier holds up the warps.  A token's
+// angles are computed once per thread, for all its rows.  Measured: 128K
+// tokens of 8 heads 93-95 us (5.7 TB/s), one row of copies at a time 104 us,
+// rows held in registers behind a block's shared table of angles 96-104 us.
+template <typename T, bool INTER, class Rows>
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm)
+    rows_kernel(const __grid_constant__ Rows rows, const ri_rope rope,
+                const int32_t* __restrict__ pos, long long pos_stride, int T_, unsigned tokens,
+                float sign, const Shape sh) {
+  constexpr int V = 16 / (int)sizeof(T);
+  constexpr int kRaws = INTER ? 1 : 2, kPairs = INTER ? V / 2 : V;
+  extern __shared__ uint4 ring_[];  // [2 kBatch][kRaws][kThreads]
+  auto ring = [&](int stage, int raw) -> uint4& {
+    return ring_[(stage * kRaws + raw) * kThreads + threadIdx.x];
+  };
   const int lane = threadIdx.x & (sh.lanes - 1), slot = threadIdx.x / sh.lanes;
   const int token_slots = kThreads / sh.lanes / sh.row_slots;
-  const int t = blockIdx.x * token_slots + slot / sh.row_slots;
-  if (t >= a.T) return;
-  const int r1 = min(a.heads, (int)(blockIdx.y + 1) * sh.group_rows);
-  for (int b = blockIdx.z; b < a.B; b += gridDim.z) {
-    const int pos = a.pos[b * a.pos_stride + t];
-    const T* x = static_cast<const T*>(a.x.data) + b * a.x.stride_b + t * a.x.stride_t;
-    T* y = static_cast<T*>(a.out.data) + b * a.out.stride_b + t * a.out.stride_t;
-    for (int i = lane; i < sh.items; i += sh.lanes) {
-      const I item(i, a.rope.rotary_dim);
-      float c[I::kPairs], s[I::kPairs];
-      item.angles(a.rope, pos, a.inverse ? -1.f : 1.f, c, s);
-      for (int r = blockIdx.y * sh.group_rows + (slot & (sh.row_slots - 1)); r < r1;
-           r += kBatch * sh.row_slots) {
-        T e[kBatch][I::kElems];
+  const unsigned tile0 = blockIdx.x * token_slots;
+  const unsigned k_step = gridDim.x * token_slots;
+  const int r0 = slot & (sh.row_slots - 1), n_rows = rows.count();
+  // (a thread without an item or a row has no tokens)
+  const unsigned k0 =
+      lane < sh.items && r0 < n_rows ? tile0 + slot / sh.row_slots : tokens;
+  const bool turns = lane < sh.turned;
+  const int n = rope.rotary_dim / 2;
+  const int at = turns ? lane * V : 2 * n + (lane - sh.turned) * V;
+
+  // the row after next ones to copy: token ki (sequence bi, token ti), row ri
+  unsigned ki = k0;
+  int bi = ki / T_, ti = ki - bi * T_, ri = r0;
+  auto copy_batch = [&](int first) {  // into slots first .. first + kBatch - 1
 #pragma unroll
-        for (int j = 0; j < kBatch; ++j)
-          if (r + j * sh.row_slots < r1)
-            item.load(x + (r + j * sh.row_slots) * a.x.stride_h, e[j]);
-#pragma unroll
-        for (int j = 0; j < kBatch; ++j)
-          if (r + j * sh.row_slots < r1) {
-            item.turn(e[j], c, s);
-            item.store(y + (r + j * sh.row_slots) * a.out.stride_h, e[j]);
+    for (int j = 0; j < kBatch; ++j)
+      if (ki < tokens) {
+        const T* src = rows.from(bi, ti, ri) + at;
+        cp_async16(&ring(first + j, 0), src);
+        if (kRaws == 2 && turns) cp_async16(&ring(first + j, kRaws - 1), src + n);
+        ri += sh.row_slots;
+        if (ri >= n_rows) {
+          ri = r0;
+          ki += k_step;
+          if (ki < tokens) {
+            bi = ki / T_;
+            ti = ki - bi * T_;
           }
+        }
+      }
+    cp_async_commit();
+  };
+  copy_batch(0);
+  int stage = 0;  // row in use, modulo 2 kBatch
+  unsigned long long turn_of[kPairs];
+#pragma unroll
+  for (int i = 0; i < kPairs; ++i)
+    turn_of[i] = turns ? __ldg(reinterpret_cast<const unsigned long long*>(rope.turns) +
+                               (INTER ? at / 2 : at) + i)
+                       : 0ull;
+  for (unsigned k = k0; k < tokens; k += k_step) {
+    const int b = k / T_, t = k - b * T_;
+    const int p = turns ? pos[b * pos_stride + t] : 0;
+    float c[kPairs], s[kPairs];
+#pragma unroll
+    for (int i = 0; i < kPairs; ++i) {
+      turn_angle(turn_of[i], p, rope.magnitude, &c[i], &s[i]);
+      s[i] *= sign;
+    }
+#pragma unroll 1
+    for (int r = r0; r < n_rows; r += sh.row_slots) {
+      if (stage % kBatch == 0) {
+        copy_batch(stage ^ kBatch);
+        cp_async_wait<1>();
+      }
+      T* dst = rows.to(b, t, r, lane == 0);
+      uint4 x = ring(stage, 0);
+      if (!turns) {
+        if (dst) *reinterpret_cast<uint4*>(dst + at) = x;
+      } else if constexpr (INTER) {
+        if (rows.turned(r)) {
+          float f[V];
+          unpack<T>(x, f);
+#pragma unroll
+          for (int i = 0; i < kPairs; ++i) {
+            const float u = f[2 * i], v = f[2 * i + 1];
+            f[2 * i] = u * c[i] - v * s[i];
+            f[2 * i + 1] = v * c[i] + u * s[i];
+          }
+          x = pack<T>(f);
+        }
+        if (dst) *reinterpret_cast<uint4*>(dst + at) = x;
+      } else {
+        uint4 y = ring(stage, kRaws - 1);
+        if (rows.turned(r)) {
+          float u[V], v[V];
+          unpack<T>(x, u);
+          unpack<T>(y, v);
+#pragma unroll
+          for (int i = 0; i < V; ++i) {
+            const float w = u[i];
+            u[i] = w * c[i] - v[i] * s[i];
+            v[i] = v[i] * c[i] + w * s[i];
+          }
+          x = pack<T>(u);
+          y = pack<T>(v);
+        }
+        if (dst) {
+          *reinterpret_cast<uint4*>(dst + at) = x;
+          *reinterpret_cast<uint4*>(dst + at + n) = y;
+        }
+      }
+      stage = (stage + 1) % (2 * kBatch);
+    }
+  }
+  cp_async_wait<0>();
+  if constexpr (Rows::kAdvances) {
+    if (rows.at_end()) {  // one token per sequence: token k is sequence k
+      __syncthreads();
+      const int H = rows.a.c.num_kv_heads;
+      for (unsigned k = tile0; k < tokens; k += k_step)
+        for (int i = threadIdx.x; i < token_slots * H; i += kThreads)
+          if (k + i / H < tokens) rows.advance((int)(k * H + i));
+    }
+  }
+}
+
+// ------------------------------------------------ any strides and alignment
+// One thread per (token, row group, element or pair): heads whose rows do not
+// start on 16 bytes, or whose halves do not.
+template <typename T, class Rows>
+__global__ void __launch_bounds__(kThreads)
+    rows_any_kernel(const __grid_constant__ Rows rows, const ri_rope rope,
+                    const int32_t* __restrict__ pos, long long pos_stride, int T_,
+                    unsigned tokens, float sign, int d, int items) {
+  const int n = rope.rotary_dim / 2, n_rows = rows.count();
+  for (unsigned k = blockIdx.x; k < tokens; k += gridDim.x) {
+    const int b = k / T_, t = k - b * T_;
+    for (int i = threadIdx.x; i < items * n_rows; i += kThreads) {
+      const int r = i / items, item = i - r * items;  // pairs first, then the rest of the head
+      const T* src = rows.from(b, t, r);
+      T* dst = rows.to(b, t, r, item == 0);
+      if (!dst) continue;
+      if (item >= n || !rows.turned(r)) {
+        if (item >= n) {
+          dst[n + item] = src[n + item];
+        } else {
+          const int ia = rope.interleaved ? 2 * item : item;
+          const int ib = rope.interleaved ? ia + 1 : item + n;
+          const T u = src[ia], v = src[ib];
+          dst[ia] = u;
+          dst[ib] = v;
+        }
+        continue;
+      }
+      float c, s;
+      turn_angle(__ldg(reinterpret_cast<const unsigned long long*>(rope.turns) + item),
+                 pos[b * pos_stride + t], rope.magnitude, &c, &s);
+      s *= sign;
+      const int ia = rope.interleaved ? 2 * item : item;
+      const int ib = rope.interleaved ? ia + 1 : item + n;
+      const float u = to_f(src[ia]), v = to_f(src[ib]);
+      dst[ia] = from_f<T>(u * c - v * s);
+      dst[ib] = from_f<T>(v * c + u * s);
+    }
+    if constexpr (Rows::kAdvances) {
+      if (rows.at_end()) {
+        __syncthreads();
+        for (int h = threadIdx.x; h < rows.a.c.num_kv_heads; h += kThreads)
+          rows.advance((int)(k * rows.a.c.num_kv_heads + h));
       }
     }
   }
 }
 
-template <typename T, int VEC, bool INTER>
-cudaError_t rotary_typed(const RotaryArgs& a, cudaStream_t s) {
-  using I = Item<T, VEC, INTER>;
-  const int n = a.rope.rotary_dim;
-  // in place the rest of the head stays where it is
-  const int items = a.x.data == a.out.data ? I::turned(n) : I::count(n, a.d);
-  const Shape sh = shape_of(items, a.T, a.B, a.heads, 1);
-  dim3 grid = grid_of(sh, a.T, a.B, a.heads);
-  if (grid.z > kMaxGridDim) grid.z = kMaxGridDim;
-  rotary_kernel<T, VEC, INTER><<<grid, kThreads, 0, s>>>(a, sh);
+// `vec`: every row and both halves start on 16 bytes.  `rest`: the elements
+// behind the turned ones are copied too.  `slot`: of the kernel in set_smem_once's table.
+template <typename T, class Rows>
+cudaError_t launch_rows(const Rows& rows, const ri_rope& rope, const int32_t* pos,
+                        long long pos_stride, int T_, int B, int d, bool inverse, bool vec,
+                        bool rest, int slot, cudaStream_t st) {
+  constexpr int V = 16 / (int)sizeof(T);
+  const unsigned tokens = (unsigned)B * T_;  // at most 2^31 (checked by the calls)
+  const float sign = inverse ? -1.f : 1.f;
+  const int rd = rope.rotary_dim;
+  if (!vec) {
+    const int items = rd / 2 + (rest ? d - rd : 0);
+    const unsigned fill = 8u * num_sms();
+    rows_any_kernel<T, Rows><<<(unsigned)(tokens < fill ? tokens : fill), kThreads, 0, st>>>(
+        rows, rope, pos, pos_stride, T_, tokens, sign, d, items);
+  } else {
+    const int turned = rope.interleaved ? rd / V : rd / 2 / V;
+    const int items = turned + (rest ? (d - rd) / V : 0);
+    const Shape sh = shape_of(turned, items, tokens, rows.count());
+    const size_t ring = 2 * kBatch * kThreads * sizeof(uint4);  // per access of a row
+    if (rope.interleaved) {
+      rows_kernel<T, true, Rows><<<sh.blocks, kThreads, ring, st>>>(rows, rope, pos, pos_stride,
+                                                                    T_, tokens, sign, sh);
+    } else {
+      const cudaError_t e = set_smem_once(
+          slot, reinterpret_cast<const void*>(rows_kernel<T, false, Rows>), (int)(2 * ring));
+      if (e != cudaSuccess) return e;
+      rows_kernel<T, false, Rows><<<sh.blocks, kThreads, 2 * ring, st>>>(
+          rows, rope, pos, pos_stride, T_, tokens, sign, sh);
+    }
+  }
   return cudaGetLastError();
 }
 
@@ -236,143 +425,44 @@ bool vec_ok(const ri_heads& x, int size) {
 }
 
 template <typename T>
-cudaError_t rotary_of(const RotaryArgs& a, cudaStream_t s) {
+cudaError_t rotary_of(const RotaryArgs& a, int slot, cudaStream_t s) {
   constexpr int V = 16 / (int)sizeof(T);
-  const bool inter = a.rope.interleaved;
-  const int run = inter ? a.rope.rotary_dim : a.rope.rotary_dim / 2;
-  // whole 16-byte accesses where every row and both halves start on one
-  const bool vec = run % V == 0 && a.d % V == 0 && a.rope.rotary_dim % V == 0 &&
+  const int rd = a.rope.rotary_dim;
+  const bool vec = (a.rope.interleaved ? rd : rd / 2) % V == 0 && a.d % V == 0 && rd % V == 0 &&
                    vec_ok(a.x, sizeof(T)) && vec_ok(a.out, sizeof(T));
-  if (vec) return inter ? rotary_typed<T, V, true>(a, s) : rotary_typed<T, V, false>(a, s);
-  return inter ? rotary_typed<T, 1, true>(a, s) : rotary_typed<T, 1, false>(a, s);
+  // in place the rest of the head stays where it is
+  return launch_rows<T>(HeadRows<T>{a}, a.rope, a.pos, a.pos_stride, a.T, a.B, a.d, a.inverse,
+                        vec, a.x.data != a.out.data, slot, s);
 }
 
-// ------------------------------------------------------------------- append
-// The rows of a token are dealt by KV head: its G query heads, its key, its
-// value.  The value's row takes the same items, copied.
-template <int VEC, bool INTER>
-__global__ void __launch_bounds__(kThreads)
-    append_kernel(const AppendTokensArgs a, const Shape sh, int advance) {
-  using T = __nv_bfloat16;
-  using I = Item<T, VEC, INTER>;
-  const int lane = threadIdx.x & (sh.lanes - 1), slot = threadIdx.x / sh.lanes;
-  const int token_slots = kThreads / sh.lanes / sh.row_slots;
-  const int t = blockIdx.x * token_slots + slot / sh.row_slots;
-  const int H = a.c.num_kv_heads, G = a.q.data ? a.c.group_size : 0, cap = a.c.capacity;
-  const int per = G + 2;  // rows of a KV head
-  const int r0 = blockIdx.y * sh.group_rows, r1 = min(H * per, r0 + sh.group_rows);
-  const int n = a.rope.turns ? a.rope.rotary_dim : 0;
-  for (int b = blockIdx.z; b < a.c.batch; b += gridDim.z) {
-    if (t < a.T) {
-      const int pos = a.pos[b * a.pos_stride + t];
-      for (int i = lane; i < sh.items; i += sh.lanes) {
-        const I item(i, n);
-        float c[I::kPairs], s[I::kPairs];
-        item.angles(a.rope, pos, 1.f, c, s);
-        for (int r = r0 + (slot & (sh.row_slots - 1)); r < r1; r += kBatch * sh.row_slots) {
-          T e[kBatch][I::kElems];
-          T* dst[kBatch];
-#pragma unroll
-          for (int j = 0; j < kBatch; ++j) {
-            const int row = r + j * sh.row_slots;
-            dst[j] = nullptr;
-            if (row >= r1) continue;
-            const int h = row / per, k = row - h * per;
-            const T* src;
-            if (k < G) {
-              src = static_cast<const T*>(a.q.data) + b * a.q.stride_b + t * a.q.stride_t +
-                    (long long)(h * G + k) * a.q.stride_h;
-              dst[j] = static_cast<T*>(a.q_out) +
-                       (((long long)b * a.T + t) * H * G + h * G + k) * kHeadDim;
-            } else {
-              const long long unit = (long long)b * H + h;
-              const int len = a.c.lens[unit];
-              const bool live = len >= 0 && len <= cap;
-              const int at = live ? len : len < 0 ? 0 : cap;
-              const bool room = at + (long long)a.T <= cap;
-              if (k == G && i == 0 && t == 0) {
-                if (!live) record_status(a.status, RI_ERR_INVALID_ARG);
-                if (!room) record_status(a.status, RI_ERR_CAPACITY);
-              }
-              if (!room) continue;
-              const ri_heads& x = k == G ? a.k : a.v;
-              src = static_cast<const T*>(x.data) + b * x.stride_b + t * x.stride_t +
-                    h * x.stride_h;
-              const long long to = unit * cap + at + t;
-              dst[j] = static_cast<T*>(k == G ? a.c.K : a.c.V) + to * kHeadDim;
-              if (k == G && i == 0) {
-                a.c.pos[to] = pos;
-                a.c.weight[to] = 0.f;
-              }
-            }
-            item.load(src, e[j]);
-          }
-#pragma unroll
-          for (int j = 0; j < kBatch; ++j)
-            if (dst[j]) {
-              const int row = r + j * sh.row_slots;
-              if (row % per != per - 1) item.turn(e[j], c, s);  // not the value
-              item.store(dst[j], e[j]);
-            }
-        }
-      }
-    }
-    if (advance) {
-      // a unit's key and value lie in one block: with one token (or lengths
-      // that go elsewhere) this block is the last to need its length
-      __syncthreads();
-      for (int h = r0 / per + threadIdx.x; h < r1 / per; h += kThreads)
-        if (blockIdx.x == 0) {
-          const int u = b * H + h, len = min(max(a.c.lens[u], 0), cap);
-          a.lens_out[u] = len + (long long)a.T <= cap ? len + a.T : len;
-        }
-    }
-  }
-}
-
-// Advances the lengths in place once every token of append_kernel is stored.
-__global__ void advance_kernel(int32_t* lens, int units, int cap, int T) {
+// The lengths after the call, once every token of it is stored.
+__global__ void advance_kernel(const StepRows rows, int units) {
   const int u = blockIdx.x * blockDim.x + threadIdx.x;
-  if (u >= units) return;
-  const int len = min(max(lens[u], 0), cap);
-  lens[u] = len + (long long)T <= cap ? len + T : len;
-}
-
-template <int VEC, bool INTER>
-cudaError_t append_typed(const AppendTokensArgs& a, cudaStream_t s) {
-  using I = Item<__nv_bfloat16, VEC, INTER>;
-  const int n = a.rope.turns ? a.rope.rotary_dim : 0;
-  const int H = a.c.num_kv_heads, per = (a.q.data ? a.c.group_size : 0) + 2;
-  const Shape sh = shape_of(I::count(n, kHeadDim), a.T, a.c.batch, H, per);
-  dim3 grid = grid_of(sh, a.T, a.c.batch, H * per);
-  if (grid.z > kMaxGridDim) grid.z = kMaxGridDim;
-  // several tokens in place: other blocks may still read a length, so a second
-  // launch advances them
-  const bool later = a.lens_out == a.c.lens && a.T > 1;
-  append_kernel<VEC, INTER><<<grid, kThreads, 0, s>>>(a, sh, !later);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess || !later) return e;
-  const int units = a.c.batch * H;
-  advance_kernel<<<(units + 255) / 256, 256, 0, s>>>(a.c.lens, units, a.c.capacity, a.T);
-  return cudaGetLastError();
+  if (u < units) rows.advance(u);
 }
 
 }  // namespace
 
 cudaError_t launch_rotary(const RotaryArgs& a, int dtype, cudaStream_t s) {
   switch (dtype) {
-    case RI_BF16: return rotary_of<__nv_bfloat16>(a, s);
-    case RI_FP16: return rotary_of<__half>(a, s);
-    default: return rotary_of<float>(a, s);
+    case RI_BF16: return rotary_of<__nv_bfloat16>(a, 8, s);
+    case RI_FP16: return rotary_of<__half>(a, 9, s);
+    default: return rotary_of<float>(a, 10, s);
   }
 }
 
 cudaError_t launch_token_append(const AppendTokensArgs& a, cudaStream_t s) {
-  const int n = a.rope.turns ? a.rope.rotary_dim : 0;
-  const bool inter = n > 0 && a.rope.interleaved;
-  const bool vec = (inter ? n : n / 2) % 8 == 0 && n % 8 == 0;
-  if (vec) return inter ? append_typed<8, true>(a, s) : append_typed<8, false>(a, s);
-  return inter ? append_typed<1, true>(a, s) : append_typed<1, false>(a, s);
+  ri_rope rope = a.rope;
+  if (!rope.turns) rope = ri_rope{nullptr, 0, 0, 1.f};  // nothing turns, all is copied
+  const int n = rope.rotary_dim, H = a.c.num_kv_heads;
+  const StepRows rows{a, a.q.data ? H * a.c.group_size : 0, a.lens_out != a.c.lens};
+  const bool vec = (rope.interleaved ? n : n / 2) % 8 == 0 && n % 8 == 0;
+  cudaError_t e = launch_rows<__nv_bfloat16>(rows, rope, a.pos, a.pos_stride, a.T, a.c.batch,
+                                             kHeadDim, false, vec, true, 11, s);
+  if (e != cudaSuccess || rows.apart || rows.at_end()) return e;
+  const int units = a.c.batch * H;
+  advance_kernel<<<(units + 255) / 256, 256, 0, s>>>(rows, units);
+  return cudaGetLastError();
 }
 
 }  // namespace ri

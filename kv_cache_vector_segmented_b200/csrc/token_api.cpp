@@ -145,6 +145,9 @@ ri_status ri_rotary(int32_t batch, int32_t tokens, int32_t heads, int32_t head_d
                     ri_stream_t stream) {
   RI_CHECK(batch >= 1 && tokens >= 1 && heads >= 1, RI_ERR_INVALID_ARG,
            "batch, tokens and heads must be >= 1 (got %d, %d, %d)", batch, tokens, heads);
+  RI_CHECK((long long)batch * tokens < 1ll << 31, RI_ERR_UNSUPPORTED,
+           "batch * tokens must be < 2^31 (got %lld)", (long long)batch * tokens);
+  RI_CHECK(heads <= 1 << 20, RI_ERR_UNSUPPORTED, "heads must be <= 2^20 (got %d)", heads);
   RI_CHECK(head_dim >= 2 && head_dim <= 256, RI_ERR_INVALID_ARG,
            "head_dim must be in [2, 256] (got %d)", head_dim);
   RI_CHECK(dtype == RI_BF16 || dtype == RI_FP16 || dtype == RI_FP32, RI_ERR_INVALID_ARG,
@@ -174,8 +177,8 @@ ri_status ri_token_append(const ri_token_cache* cache, int32_t tokens, const ri_
   ri_status st = check_arrays(cache, "token cache");
   if (st != RI_OK) return st;
   RI_CHECK(tokens >= 1, RI_ERR_INVALID_ARG, "tokens must be >= 1 (got %d)", tokens);
-  RI_CHECK((long long)cache->batch * cache->num_kv_heads * tokens <= 1ll << 33,
-           RI_ERR_UNSUPPORTED, "batch * num_kv_heads * tokens must be <= 2^33");
+  RI_CHECK((long long)cache->batch * tokens < 1ll << 31, RI_ERR_UNSUPPORTED,
+           "batch * tokens must be < 2^31 (got %lld)", (long long)cache->batch * tokens);
   if ((st = check_rows(k, "k")) != RI_OK || (st = check_rows(v, "v")) != RI_OK) return st;
   RI_CHECK(pos && aligned4(pos), RI_ERR_INVALID_ARG, "pos must be non-NULL and 4-byte aligned");
   if (rope && (st = check_rope(rope, 128)) != RI_OK) return st;
