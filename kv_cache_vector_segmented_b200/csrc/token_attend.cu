@@ -932,23 +932,52 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
 // the shares, whose factors 2^(m - M) stay in shared memory); the unit's
 // blocks share out the rows' numerators, four columns per lane.
 constexpr int kMergeThreads = 256;
-constexpr int kMergeTokens = 4 * kMergeThreads;  // own tokens of a chunk
+constexpr int kMergeTokens = 4 * kMergeThreads;  // own tokens of a chunk, at least
 
-__global__ void __launch_bounds__(kMergeThreads)
+// log2 scores of one own token, Gp = 4 or 8 of them
+struct Scores {
+  float4 a, b;
+};
+__device__ __forceinline__ Scores load_scores(const AttendParams& p, size_t row, int G) {
+  const float4* s = reinterpret_cast<const float4*>(p.score) + row * (G <= 4 ? 1 : 2);
+  Scores r;
+  r.a = s[0];
+  r.b = G > 4 ? s[1] : make_float4(0.f, 0.f, 0.f, 0.f);
+  return r;
+}
+
+__global__ void __launch_bounds__(kMergeThreads, 4)
     merge_kernel(const __grid_constant__ AttendParams p, int chunks) {
   extern __shared__ float factor[];  // [G][shares]
   __shared__ float sh_lse[kMaxGroup], sh_l[kMaxGroup];
   __shared__ int sh_n[kMaxGroup], sh_slot[kMaxGroup];  // prefix shares, the first one's slot
   __shared__ float4 sh_part[kMergeThreads / 32][32];
   const int unit = blockIdx.x / chunks, chunk = blockIdx.x - unit * chunks;
-  const int G = p.c.group_size, H = p.c.num_kv_heads, Gp = G <= 4 ? 4 : 8;
+  const int G = p.c.group_size, H = p.c.num_kv_heads;
   const int b = unit / H, h = unit - b * H;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const PrefixPlan& plan = p.plan;
   const int shares = plan.blocks + p.splits;  // room per row; most rows use fewer
+  // (the lengths are older than the two launches before this one)
+  const int len = live_len(p.c, unit, p.status);
+  const int per_chunk = (p.c.capacity + chunks - 1) / chunks;
+  const int i0 = chunk * per_chunk + threadIdx.x;
+  const int end = p.add_weight ? min(len, (chunk + 1) * per_chunk) : 0;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (blockIdx.x == 0 && threadIdx.x == 0) *p.next_task = 0;  // every task has been taken
-  const int len = live_len(p.c, unit, p.status);
+  // the first own tokens' scores and weights, on their way meanwhile
+  constexpr int kAhead = 2;
+  const size_t row0 = (size_t)unit * p.c.capacity;
+  Scores ahead[kAhead];
+  float weight[kAhead];
+#pragma unroll
+  for (int j = 0; j < kAhead; ++j) {
+    const int i = i0 + j * kMergeThreads;
+    if (i < end) {
+      ahead[j] = load_scores(p, row0 + i, G);
+      weight[j] = p.c.weight[row0 + i];
+    }
+  }
   if (warp < G) {
     const int g = warp, r = b * G + g, row = r % kTile;
     int c0 = 0, n_prefix = 0, u = 0, slot = 0;
@@ -997,7 +1026,8 @@ __global__ void __launch_bounds__(kMergeThreads)
   }
   __syncthreads();
   // The numerators: row g is joined by block g mod chunks of the unit, by
-  // `per_row` warps that take its shares in turn, eight loads in flight each.
+  // `per_row` warps that take its shares in turn, kFlight loads in flight each.
+  constexpr int kFlight = 4;
   const int rows_here = chunk < G ? (G - chunk + chunks - 1) / chunks : 0;
   if (rows_here) {
     const int per_row = rows_here <= 1 ? 8 : rows_here <= 2 ? 4 : rows_here <= 4 ? 2 : 1;
@@ -1010,12 +1040,12 @@ __global__ void __launch_bounds__(kMergeThreads)
                              ((size_t)sh_slot[g] * kTile + (b * G + g) % kTile) * (kD / 4) + lane;
       const float4* own = reinterpret_cast<const float4*>(p.num) +
                           ((size_t)unit * p.splits * G + g) * (kD / 4) + lane;
-      for (int i0 = part; i0 < all; i0 += 8 * per_row) {
-        float4 v[8];
-        float w[8];
+      for (int f0 = part; f0 < all; f0 += kFlight * per_row) {
+        float4 v[kFlight];
+        float w[kFlight];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int i = i0 + j * per_row;
+        for (int j = 0; j < kFlight; ++j) {
+          const int i = f0 + j * per_row;
           w[j] = i < all ? f[i] : 0.f;
           v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
           // factor 0: nothing was written there, or nothing that counts
@@ -1024,7 +1054,7 @@ __global__ void __launch_bounds__(kMergeThreads)
                            : own + (size_t)(i - n) * G * (kD / 4));
         }
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int j = 0; j < kFlight; ++j) {
           acc.x = fmaf(w[j], v[j].x, acc.x);
           acc.y = fmaf(w[j], v[j].y, acc.y);
           acc.z = fmaf(w[j], v[j].z, acc.z);
@@ -1052,29 +1082,29 @@ __global__ void __launch_bounds__(kMergeThreads)
       if (p.lse && lane == 0) p.lse[row] = sh_lse[g] * kLn2;
     }
   }
-  if (!p.add_weight) return;
+  if (i0 >= end) return;
   float lse[kMaxGroup];
 #pragma unroll
   for (int g = 0; g < kMaxGroup; ++g) lse[g] = g < G ? sh_lse[g] : 0.f;
-  const int end = min(len, (chunk + 1) * kMergeTokens);
-#pragma unroll 4
-  for (int i = chunk * kMergeTokens + threadIdx.x; i < end; i += kMergeThreads) {
-    const size_t row = (size_t)unit * p.c.capacity + i;
-    const float4* s = reinterpret_cast<const float4*>(p.score + row * Gp);
-    const float4 a = s[0];
-    float w = exp2_approx(a.x - lse[0]);
-    if (G > 1) w += exp2_approx(a.y - lse[1]);
-    if (G > 2) w += exp2_approx(a.z - lse[2]);
-    if (G > 3) w += exp2_approx(a.w - lse[3]);
-    if (G > 4) {
-      const float4 e = s[1];
-      w += exp2_approx(e.x - lse[4]);
-      if (G > 5) w += exp2_approx(e.y - lse[5]);
-      if (G > 6) w += exp2_approx(e.z - lse[6]);
-      if (G > 7) w += exp2_approx(e.w - lse[7]);
-    }
-    p.c.weight[row] += w;
+  auto added = [&](const Scores& s) {  // (entries from G on were never written)
+    float w = exp2_approx(s.a.x - lse[0]);
+    if (G > 1) w += exp2_approx(s.a.y - lse[1]);
+    if (G > 2) w += exp2_approx(s.a.z - lse[2]);
+    if (G > 3) w += exp2_approx(s.a.w - lse[3]);
+    if (G > 4) w += exp2_approx(s.b.x - lse[4]);
+    if (G > 5) w += exp2_approx(s.b.y - lse[5]);
+    if (G > 6) w += exp2_approx(s.b.z - lse[6]);
+    if (G > 7) w += exp2_approx(s.b.w - lse[7]);
+    return w;
+  };
+#pragma unroll
+  for (int j = 0; j < kAhead; ++j) {
+    const int i = i0 + j * kMergeThreads;
+    if (i < end) p.c.weight[row0 + i] = weight[j] + added(ahead[j]);
   }
+#pragma unroll 2
+  for (int i = i0 + kAhead * kMergeThreads; i < end; i += kMergeThreads)
+    p.c.weight[row0 + i] += added(load_scores(p, row0 + i, G));
 }
 
 // --------------------------------------------------------------------- host
@@ -1177,7 +1207,10 @@ cudaError_t launch_token_attend(const TokenAttendArgs& a, cudaStream_t s) {
   e = launch_dependent(own_kernel, want < fill ? want : fill, kOwnThreads, kOwnSmem, s,
                        p.plan.blocks > 0, p);
   if (e == cudaSuccess) {
-    const int chunks = a.add_weight ? (a.c.capacity + kMergeTokens - 1) / kMergeTokens : 1;
+    // about one round of blocks, four per SM, of kMergeTokens own tokens or more
+    int chunks = a.add_weight ? (a.c.capacity + kMergeTokens - 1) / kMergeTokens : 1;
+    const int most = 4 * num_sms() / units;
+    if (chunks > most) chunks = most > 1 ? most : 1;
     const size_t smem = (size_t)a.c.group_size * (p.plan.blocks + L.splits) * sizeof(float);
     e = launch_dependent(merge_kernel, units * chunks, kMergeThreads, smem, s, true, p, chunks);
   }
