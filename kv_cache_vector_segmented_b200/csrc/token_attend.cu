@@ -383,6 +383,8 @@ __device__ __forceinline__ int take_task(const AttendParams& p) {
 __global__ void __launch_bounds__(kOwnThreads)
     own_kernel(const __grid_constant__ AttendParams p) {
   extern __shared__ __align__(128) uint8_t smem[];
+  // behind a prefix launch everything older is complete (it has waited)
+  if (!p.plan.blocks) asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int warp = threadIdx.x >> 5;
   const uint32_t buf = smem_u32(smem) + warp * own_ring_bytes(kOwnStages);
@@ -398,7 +400,9 @@ __global__ void __launch_bounds__(kOwnThreads)
 }
 
 // ------------------------------------------------------------ prefix kernel
-constexpr int kRing = 4;                  // K / V tiles in flight
+// K / V tiles in flight: 4 beside two query tiles; with one row tile per KV
+// head (the memory-bound case) the second query tile's room is a fifth
+constexpr int kRingPair = 4, kRingSingle = 5;
 constexpr int kSoftmaxWarps = 8;          // two warpgroups, one per slot
 constexpr int kWarpMma = 8, kWarpLoad = 9;
 constexpr int kWarpOwn = 10;              // warps 10 and 11: own tokens meanwhile
@@ -412,12 +416,12 @@ constexpr int kRegsSoftmax = 192, kRegsRest = 112;
 constexpr uint32_t kColS = 0, kColO = 256;
 
 struct PrefixShared {
-  uint64_t full[kRing], empty[kRing];
+  uint64_t full[kRingSingle], empty[kRingSingle];
   uint64_t q_full, s_full[2], p_full[2][2], o_full[2], drain;
   uint32_t tmem;
   int done;  // the block's prefix work is through: no more own shares are taken
 };
-constexpr size_t kPrefixSmem = 1024 + (2 + kRing) * (size_t)kTileBytes +
+constexpr size_t kPrefixSmem = 1024 + (2 + kRingPair) * (size_t)kTileBytes +
                                2 * own_ring_bytes(kOwnStagesBeside) + sizeof(PrefixShared);
 
 // V tile [key][d] as the B operand of num += P V (N = d contiguous, "MN
@@ -485,32 +489,35 @@ struct Share {
   bool pair;
 };
 
+template <int kQTiles>
 __device__ __forceinline__ Share share_of(const PrefixPlan& p, int u, int x0, int x1) {
   Share s;
   s.head = u / p.per_head;
   s.row0 = (u % p.per_head) * 2 * kTile;
   s.t0 = p.tile_at(u, x0);
   s.t1 = p.tile_at(u, x1);
-  s.pair = p.work_per_tile(u) == 2;
+  s.pair = kQTiles == 2 && p.work_per_tile(u) == 2;
   return s;
 }
 
+template <int kRing>
 __global__ void __launch_bounds__(kPrefixThreads, 1)
     prefix_kernel(const __grid_constant__ CUtensorMap map_k,
                   const __grid_constant__ CUtensorMap map_v,
                   const __grid_constant__ AttendParams p) {
   extern __shared__ uint8_t raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~1023ull);
-  uint8_t* sq = base;                       // 2 query tiles
-  uint8_t* ring = base + 2 * kTileBytes;    // kRing K / V tiles
-  uint8_t* own = ring + kRing * kTileBytes; // the rings of warps 10 and 11
+  constexpr int kQTiles = kRing == kRingSingle ? 1 : 2;
+  static_assert(kQTiles + kRing == 2 + kRingPair, "one layout of shared memory");
+  uint8_t* sq = base;                             // kQTiles query tiles
+  uint8_t* ring = base + kQTiles * kTileBytes;    // kRing K / V tiles
+  uint8_t* own = ring + kRing * kTileBytes;       // the rings of warps 10 and 11
   PrefixShared* sh =
       reinterpret_cast<PrefixShared*>(own + 2 * own_ring_bytes(kOwnStagesBeside));
   // (shuffled: uniform over the warp for the compiler too)
   const int tid = threadIdx.x, warp = __shfl_sync(~0u, tid >> 5, 0), lane = tid & 31;
   const PrefixPlan& plan = p.plan;
 
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (warp == kWarpMma) {
     tmem_alloc(&sh->tmem, 512);
     tmem_relinquish();
@@ -535,6 +542,10 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(~0u, sh->tmem, 0);
+  // what came before on the stream is complete from here on; only then may
+  // the own tokens' launch start, which reads what that wrote without a wait
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   const int x0 = plan.from(blockIdx.x), x1 = plan.from(blockIdx.x + 1);
   const int u0 = plan.unit_of(x0);
@@ -566,7 +577,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
           ++n;
         };
         for (int u = u0; u < plan.units && plan.start(u) < x1; ++u) {
-          const Share s = share_of(plan, u, x0, x1);
+          const Share s = share_of<kQTiles>(plan, u, x0, x1);
           const int ahead = s.pair ? 1 : 2;  // key tiles before the first value tile
           for (int t = s.t0; t < s.t1 && t < s.t0 + ahead; ++t) load(&map_k, t, s.head);
           for (int t = s.t0; t < s.t1; ++t) {
@@ -641,7 +652,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
         };
         auto release = [&](int i) { commit(&sh->empty[i % kRing]); };
         for (int u = u0; u < plan.units && plan.start(u) < x1; ++u) {
-          const Share s = share_of(plan, u, x0, x1);
+          const Share s = share_of<kQTiles>(plan, u, x0, x1);
           const int T = s.t1 - s.t0;
           if (T <= 0) continue;
           wait(&sh->q_full, q_phase);
@@ -712,14 +723,14 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
     const uint32_t lane_addr = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t t_s = tmem + lane_addr + kColS + slot * kTile;
     const uint32_t t_o = tmem + lane_addr + kColO + slot * kD;
-    uint32_t s_phase = 0, o_phase = 0;
+    uint32_t s_phase = 0, o_phase = 0, unit_phase = 0;  // unit: of o_full[0]
     const int H = p.c.num_kv_heads, G = p.c.group_size;
     auto wait = [&](uint64_t* bar, uint32_t parity) {
       if (ok) ok = __all_sync(~0u, mbar_wait(bar, parity));
       if (!ok && lane == 0) record_status(p.status, RI_ERR_TIMEOUT);
     };
     for (int u = u0; u < plan.units && plan.start(u) < x1; ++u) {
-      const Share s = share_of(plan, u, x0, x1);
+      const Share s = share_of<kQTiles>(plan, u, x0, x1);
       const int T = s.t1 - s.t0;
       if (T <= 0) continue;
       // the unit's query rows, into the K-major 128-byte swizzle: a thread
@@ -840,23 +851,27 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
         wait(&sh->o_full[slot], o_phase);
         o_phase ^= 1;
       }
-      // Through shared memory (the query tiles are free: 8 KB per warp), so
-      // that rows leave as whole 256-byte pieces: a thread holds a row, and 32
-      // rows' 16-byte stores would each touch 32 lines.
+      // Through shared memory (the query tiles are free: an equal part per
+      // warp), so that rows leave as whole 128- or 256-byte pieces: a thread
+      // holds a row, and 32 rows' 16-byte stores would each touch 32 lines.
+      constexpr int kCols = 32 * kQTiles, kChunks = kCols / 4;  // columns at a time
       const size_t out_slot = 2 * ((size_t)blockIdx.x + u) + (s.pair ? slot : 0);
       float* num = p.pnum + out_slot * kTile * kD;
       float* ml = p.pml + out_slot * kTile * 2;
-      uint8_t* stage = sq + warp * 8192;
+      uint8_t* stage = sq + warp * (32 * kCols * 4);
       const int warp_row = (warp & 3) * 32;
       const int n_rows = min(32, plan.rows - row_tile0 - warp_row);  // <= 0: none live
       auto put = [&](int i, uint4 v) {  // 16-byte chunk i of this thread's row
-        *reinterpret_cast<uint4*>(stage + lane * 256 + ((i ^ (lane & 15)) << 4)) = v;
+        *reinterpret_cast<uint4*>(stage + lane * (kCols * 4) +
+                                  ((i ^ (lane & (kChunks - 1))) << 4)) = v;
       };
-      auto send = [&](int half) {  // 64 columns of the warp's rows
+      auto send = [&](int col) {  // the warp's rows, kCols columns from col on
         __syncwarp();
-        for (int r = lane >> 4; r < n_rows; r += 2)
-          *reinterpret_cast<uint4*>(num + (warp_row + r) * kD + half * 64 + (lane & 15) * 4) =
-              *reinterpret_cast<const uint4*>(stage + r * 256 + (((lane & 15) ^ (r & 15)) << 4));
+        const int c = lane & (kChunks - 1);
+        for (int r = lane / kChunks; r < n_rows; r += 32 / kChunks)
+          *reinterpret_cast<uint4*>(num + (warp_row + r) * kD + col + c * 4) =
+              *reinterpret_cast<const uint4*>(stage + r * (kCols * 4) +
+                                              ((c ^ (r & (kChunks - 1))) << 4));
         __syncwarp();
       };
       if (s.pair) {
@@ -865,24 +880,25 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
           tc_fence_after();
           if (lane < n_rows) *reinterpret_cast<float2*>(ml + row * 2) = make_float2(m, l);
 #pragma unroll 1
-          for (int half = 0; half < 2; ++half) {
-            uint32_t a[32], b[32];
-            tmem_ld32_nowait(t_o + half * 64, a);
-            tmem_ld32_nowait(t_o + half * 64 + 32, b);
+          for (int c = 0; c < 4; ++c) {
+            uint32_t a[32];
+            tmem_ld32_nowait(t_o + c * 32, a);
             tmem_wait_ld();
+            const int part = c * 32 % kCols / 4;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              put(i, make_uint4(a[4 * i], a[4 * i + 1], a[4 * i + 2], a[4 * i + 3]));
-              put(8 + i, make_uint4(b[4 * i], b[4 * i + 1], b[4 * i + 2], b[4 * i + 3]));
-            }
-            send(half);
+            for (int i = 0; i < 8; ++i)
+              put(part + i, make_uint4(a[4 * i], a[4 * i + 1], a[4 * i + 2], a[4 * i + 3]));
+            if ((c + 1) * 32 % kCols == 0) send((c + 1) * 32 - kCols);
           }
           tc_fence_before();
         }
       } else {
         // both slots hold the same rows: (m, l) change hands, and each
         // warpgroup joins half of the columns of both numerators
-        float2* ex = reinterpret_cast<float2*>(sq + kTileBytes);  // [2][128]
+        // (a slot without a tile waits for the other's products, which read
+        // the query tile this goes over)
+        if (!used) wait(&sh->o_full[0], unit_phase);
+        float2* ex = reinterpret_cast<float2*>(sq);  // [2][128]
         ex[slot * kTile + row] = used ? make_float2(m, l) : make_float2(-INFINITY, 0.f);
         named_barrier(1, kSoftmaxWarps * 32);
         const float2 e0 = ex[row], e1 = ex[kTile + row];
@@ -909,15 +925,17 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
             }
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-              put(c * 8 + i, make_uint4(a[4 * i], a[4 * i + 1], a[4 * i + 2], a[4 * i + 3]));
+              put(c * 32 % kCols / 4 + i,
+                  make_uint4(a[4 * i], a[4 * i + 1], a[4 * i + 2], a[4 * i + 3]));
+            if ((c + 1) * 32 % kCols == 0) send(slot * 64 + (c + 1) * 32 - kCols);
           }
-          send(slot);
           tc_fence_before();
         }
       }
       // the numerators are read and the query tiles done with (their last
       // scores were waited for) before the next unit replaces either
       named_barrier(1, kSoftmaxWarps * 32);
+      unit_phase ^= 1;
     }
     if (tid == 0) *reinterpret_cast<volatile int*>(&sh->done) = 1;
   }
@@ -1146,7 +1164,7 @@ cudaError_t encode_prefix(CUtensorMap* map, const void* base, const ri_token_pre
 
 template <typename... Args, typename... Given>
 cudaError_t launch_dependent(void (*kernel)(Args...), int blocks, int threads, size_t smem,
-                             cudaStream_t s, bool dependent, const Given&... args) {
+                             cudaStream_t s, const Given&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)blocks);
   cfg.blockDim = dim3((unsigned)threads);
@@ -1156,7 +1174,7 @@ cudaError_t launch_dependent(void (*kernel)(Args...), int blocks, int threads, s
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = dependent ? 1 : 0;
+  cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
@@ -1193,26 +1211,30 @@ cudaError_t launch_token_attend(const TokenAttendArgs& a, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   if (p.plan.blocks) {
     CUtensorMap mk, mv;
-    e = set_smem_once(4, reinterpret_cast<const void*>(prefix_kernel), (int)kPrefixSmem);
+    const bool single = p.plan.tiles == 1;
+    void (*kernel)(CUtensorMap, CUtensorMap, AttendParams) =
+        single ? prefix_kernel<kRingSingle> : prefix_kernel<kRingPair>;
+    e = set_smem_once(single ? 4 : 12, reinterpret_cast<const void*>(kernel), (int)kPrefixSmem);
     if (e == cudaSuccess) e = encode_prefix(&mk, a.p.K, a.p, a.c.num_kv_heads);
     if (e == cudaSuccess) e = encode_prefix(&mv, a.p.V, a.p, a.c.num_kv_heads);
+    if (e == cudaSuccess)
+      e = launch_dependent(kernel, p.plan.blocks, kPrefixThreads, kPrefixSmem, s, mk, mv, p);
     if (e != cudaSuccess) return e;
-    prefix_kernel<<<p.plan.blocks, kPrefixThreads, kPrefixSmem, s>>>(mk, mv, p);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
-  // The prefix launch is ordered like any other; the two after it may start
-  // while it runs (programmatic dependent launch): the own tokens' blocks
-  // take the SMs that it leaves, the merge waits for both.
+  // Every launch sets up while the one before it ends (programmatic dependent
+  // launch).  Behind a prefix the own tokens' blocks take the SMs that it
+  // leaves; the merge waits for both.
   const int fill = 2 * num_sms(), want = (p.tasks + kOwnWarps - 1) / kOwnWarps;
-  e = launch_dependent(own_kernel, want < fill ? want : fill, kOwnThreads, kOwnSmem, s,
-                       p.plan.blocks > 0, p);
+  e = launch_dependent(own_kernel, want < fill ? want : fill, kOwnThreads, kOwnSmem, s, p);
   if (e == cudaSuccess) {
-    // about one round of blocks, four per SM, of kMergeTokens own tokens or more
+    // about one round of blocks, four per SM: a block per row of the group, or
+    // per kMergeTokens own tokens, while there is room
     int chunks = a.add_weight ? (a.c.capacity + kMergeTokens - 1) / kMergeTokens : 1;
+    if (chunks < a.c.group_size) chunks = a.c.group_size;
     const int most = 4 * num_sms() / units;
     if (chunks > most) chunks = most > 1 ? most : 1;
     const size_t smem = (size_t)a.c.group_size * (p.plan.blocks + L.splits) * sizeof(float);
-    e = launch_dependent(merge_kernel, units * chunks, kMergeThreads, smem, s, true, p, chunks);
+    e = launch_dependent(merge_kernel, units * chunks, kMergeThreads, smem, s, p, chunks);
   }
   // without its merge a prefix launch leaves the counter standing
   if (e != cudaSuccess && p.plan.blocks) cudaMemsetAsync(p.next_task, 0, sizeof(int), s);
