@@ -5,9 +5,9 @@
 // The order is total: held tokens (first and most recent positions) before
 // all others, then larger weight, then lower row.  A token's rank is a 32-bit
 // key (the order-preserving image of its weight, all ones when held).  The
-// keep-th token is found by counting: the keys' range is cut into 512 equal
-// buckets, the bucket that holds the keep-th key is cut again while it has
-// more than 512 keys (once in all is usual: a float's bits spread the weights
+// keep-th token is found by counting: the keys' range is cut into 1024
+// equal buckets, the bucket that holds the keep-th key is cut again while it
+// has more than 256 keys (once in all is usual: a float's bits spread the weights
 // over the range by their logarithm), and its keys are then ranked one
 // against the other.  Every step is a count, a prefix sum or a comparison:
 // the result does not depend on the order in which threads run.
@@ -24,12 +24,14 @@ namespace ri {
 
 namespace {
 
-constexpr int kThreads = 512;  // two blocks per SM at 64 registers
+constexpr int kThreads = 1024;
+constexpr int kBucketBits = 10;  // 1 << kBucketBits == kThreads
 constexpr int kWarps = kThreads / 32;
+constexpr int kRowsPerThread = 2;
 constexpr int kMaxCluster = 16;
 // rows whose keys and positions a block holds (8 bytes each); a longer slice
 // (caches of more than 16 x this) is read again from global memory instead
-constexpr int kMaxHeld = 24576;
+constexpr int kMaxHeld = 23552;
 
 struct EvictParams {
   ri_token_cache c, o;
@@ -48,8 +50,10 @@ __device__ __forceinline__ uint32_t rank_key(float w, int pos, int first, long l
 }
 
 constexpr int kBuckets = kThreads;  // one thread sums one bucket
-constexpr int kPasses = 4;          // 9 bits each, of 32
-constexpr int kRanked = kThreads;   // most candidates ranked directly
+constexpr int kPasses = 4;          // kBucketBits each, of 32
+static_assert(kBuckets == 1 << kBucketBits, "");
+constexpr int kRanked = 256;        // most candidates ranked directly, by four threads each
+static_assert(kThreads == 4 * kRanked, "");
 
 // Shared memory every block of a cluster may read.
 struct Exchange {
@@ -117,7 +121,7 @@ __device__ __forceinline__ int warps_before(int count, int* sums, int* all) {
 
 // kHeld: the slice's keys stay in shared memory.
 template <bool kHeld>
-__global__ void __launch_bounds__(kThreads, 2) evict_kernel(const __grid_constant__ EvictParams p) {
+__global__ void __launch_bounds__(kThreads) evict_kernel(const __grid_constant__ EvictParams p) {
   // kHeld: the slice's keys, its positions; then one bit per row
   extern __shared__ uint32_t held[];
   __shared__ Exchange x;
@@ -199,7 +203,7 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const __grid_constan
 
     // ---- the bucket of the keep-th key, narrowed down
     const uint32_t span = high - low;
-    int shift = span < kBuckets ? 0 : 32 - __clz(span) - 9;  // span >> shift < 512
+    int shift = span < kBuckets ? 0 : 32 - __clz(span) - kBucketBits;  // span >> shift < kBuckets
     uint32_t range = span;  // keys of interest: low .. low + range
     int above = 0, count = 0;
 #pragma unroll 1
@@ -229,7 +233,7 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const __grid_constan
         above = 0;
         break;
       }
-      // thread t sums bucket 511 - t, so that a prefix sum runs from the top
+      // thread t sums bucket kBuckets - 1 - t, so that a prefix sum runs from the top
       int v[kMaxCluster], sum = 0;
 #pragma unroll
       for (int b = 0; b < kMaxCluster; ++b)
@@ -256,7 +260,7 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const __grid_constan
       count = x.count;
       range = (1u << shift) - 1;  // of this bucket
       if (count <= kRanked || shift == 0) break;
-      shift = shift > 9 ? shift - 9 : 0;
+      shift = shift > kBucketBits ? shift - kBucketBits : 0;
     }
     const int need = keep - above;  // of the bucket's keys, in order
 
@@ -275,12 +279,14 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const __grid_constan
         first += nb;
       }
       __syncthreads();
-      if (tid < count) {
-        const unsigned long long me = x.all[tid];
+      {
+        const unsigned long long me = (tid >> 2) < count ? x.all[tid >> 2] : 0ull;
         int larger = 0;
 #pragma unroll 4
-        for (int j = 0; j < count; ++j) larger += x.all[j] > me;
-        if (larger == need - 1) {
+        for (int j = tid & 3; j < count; j += 4) larger += x.all[j] > me;
+        larger += __shfl_xor_sync(~0u, larger, 1);
+        larger += __shfl_xor_sync(~0u, larger, 2);
+        if ((tid >> 2) < count && (tid & 3) == 0 && larger == need - 1) {
           x.cut_key = (uint32_t)(me >> 32);
           x.above = (int)~(uint32_t)me;  // its row
         }
@@ -445,11 +451,12 @@ cudaError_t launch_token_evict(const TokenEvictArgs& a, cudaStream_t s) {
   const int cap = a.c.capacity, W = a.budget < cap ? a.budget : cap;
   p.holes = reinterpret_cast<int32_t*>(a.ws + kStatusBytesHost);
   p.moved = p.holes + (size_t)units * W;
-  // Blocks per unit: more while a block has over 4 rows per thread and the
-  // grid is within two blocks per SM.
+  // Blocks per unit: more while a block has over kRowsPerThread rows per thread
+  // and the grid is within a block per SM.
+  // (of 8 at most, which any GPC holds twice, unless the slices get too long)
   int cluster = 1;
-  while (cluster < kMaxCluster && cap > cluster * 4 * kThreads &&
-         (long long)units * cluster * 2 <= 2 * num_sms())
+  while (cluster < 8 && cap > cluster * kRowsPerThread * kThreads &&
+         (long long)units * cluster * 2 <= num_sms())
     cluster *= 2;
   while (cluster < kMaxCluster && cap > (long long)cluster * (kMaxHeld - 32)) cluster *= 2;
   p.cluster = cluster;
