@@ -27,7 +27,10 @@ namespace {
 constexpr int kThreads = 1024;
 constexpr int kBucketBits = 10;  // 1 << kBucketBits == kThreads
 constexpr int kWarps = kThreads / 32;
+constexpr int kMoveThreads = 256;
 constexpr int kRowsPerThread = 2;
+// rows per unit from which a launch of its own for the moves pays
+constexpr int kApartRows = 2048;
 constexpr int kMaxCluster = 16;
 // rows whose keys and positions a block holds (8 bytes each); a longer slice
 // (caches of more than 16 x this) is read again from global memory instead
@@ -39,6 +42,8 @@ struct EvictParams {
   int cluster;     // blocks per unit
   int32_t* holes;  // [units][W]: rows below keep whose tokens are dropped, in order
   int32_t* moved;  // [units][W]: rows from keep on whose tokens stay, in order
+  int32_t* listed; // [units]: rows to move; -n: rows 0 .. n - 1, each to its own number
+  bool apart;      // a second launch moves the rows
   int* status;
 };
 
@@ -119,11 +124,56 @@ __device__ __forceinline__ int warps_before(int count, int* sums, int* all) {
   return __shfl_sync(~0u, x - v, warp);
 }
 
+// Row moved[k] -> row holes[k] of a unit, for the rows of one warp of `warps`:
+// up to 32 in a row, their numbers in one load, their K and V eight rows in
+// flight.  Sources of moves lie at or behind keep, destinations before it: no
+// move reads what another writes.
+__device__ __forceinline__ void move_rows(const EvictParams& p, int unit, int n_rows, int warp,
+                                          int warps) {
+  const int lane = threadIdx.x & 31, ch = lane & 15;
+  const int cap = p.c.capacity, W = min(p.budget, cap);
+  const bool list = n_rows >= 0;
+  if (!list) n_rows = -n_rows;
+  const int32_t* holes = p.holes + (size_t)unit * W;
+  const int32_t* moved = p.moved + (size_t)unit * W;
+  const size_t src0 = (size_t)unit * cap, dst0 = (size_t)unit * p.o.capacity;
+  const int32_t* pos = p.c.pos + src0;
+  const float* weight = p.c.weight + src0;
+  const bool pos_apart = p.c.pos != p.o.pos, weight_apart = p.c.weight != p.o.weight;
+  const uint4* kv_src = reinterpret_cast<const uint4*>(lane < 16 ? p.c.K : p.c.V);
+  uint4* kv_dst = reinterpret_cast<uint4*>(lane < 16 ? p.o.K : p.o.V);
+  const int run = min(32, (n_rows + warps - 1) / warps);
+  for (int k0 = warp * run; k0 < n_rows; k0 += warps * run) {
+    const int n = min(run, n_rows - k0);
+    int from = 0, to = 0;
+    if (lane < n) {
+      from = list ? moved[k0 + lane] : k0 + lane;
+      to = list ? holes[k0 + lane] : k0 + lane;
+      if (from != to || pos_apart) p.o.pos[dst0 + to] = pos[from];
+      if (from != to || weight_apart) p.o.weight[dst0 + to] = weight[from];
+    }
+    for (int j0 = 0; j0 < n; j0 += 8) {
+      uint4 v[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int f = __shfl_sync(~0u, from, j0 + j);
+        if (j0 + j < n) v[j] = kv_src[(src0 + f) * 16 + ch];
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int d = __shfl_sync(~0u, to, j0 + j);
+        if (j0 + j < n) kv_dst[(dst0 + d) * 16 + ch] = v[j];
+      }
+    }
+  }
+}
+
 // kHeld: the slice's keys stay in shared memory.
 template <bool kHeld>
 __global__ void __launch_bounds__(kThreads) evict_kernel(const __grid_constant__ EvictParams p) {
   // kHeld: the slice's keys, its positions; then one bit per row
   extern __shared__ uint32_t held[];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   __shared__ Exchange x;
   const int n_blocks = p.cluster;
   const int unit = blockIdx.x / n_blocks, rank = blockIdx.x - unit * n_blocks;
@@ -380,7 +430,7 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const __grid_constant__
   unit_sync(n_blocks);
   if (rank == 0 && tid == 0) p.o.lens[unit] = keep;
 
-  const size_t src0 = (size_t)unit * cap, dst0 = (size_t)unit * p.o.capacity;
+  const size_t dst0 = (size_t)unit * p.o.capacity;
   const bool pos_apart = p.c.pos != p.o.pos, weight_apart = p.c.weight != p.o.weight;
   // ---- positions and weights of rows that stay, where only these are apart
   if (!kv_apart && (pos_apart || weight_apart)) {
@@ -395,40 +445,21 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const __grid_constant__
       }
     }
   }
-  // ---- row moved[k] -> row holes[k]: a warp takes up to 32 in a row, their
-  // numbers in one load, their K and V eight rows in flight.  Sources of moves
-  // lie at or behind keep, destinations before it: no move reads what another
-  // writes.
-  const uint4* kv_src = reinterpret_cast<const uint4*>(lane < 16 ? p.c.K : p.c.V);
-  uint4* kv_dst = reinterpret_cast<uint4*>(lane < 16 ? p.o.K : p.o.V);
-  const int ch = lane & 15;
-  const int warps = n_blocks * kWarps;
   // (nothing leaves: the rows are their own list)
-  const int n_rows = kv_apart ? keep : n_moves;
-  const int run = min(32, (n_rows + warps - 1) / warps);
-  for (int k0 = (rank * kWarps + warp) * run; k0 < n_rows; k0 += warps * run) {
-    const int n = min(run, n_rows - k0);
-    int from = 0, to = 0;
-    if (lane < n) {
-      from = leaves ? moved[k0 + lane] : k0 + lane;
-      to = leaves ? holes[k0 + lane] : k0 + lane;
-      if (from != to || pos_apart) p.o.pos[dst0 + to] = pos[from];
-      if (from != to || weight_apart) p.o.weight[dst0 + to] = weight[from];
-    }
-    for (int j0 = 0; j0 < n; j0 += 8) {
-      uint4 v[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int f = __shfl_sync(~0u, from, j0 + j);
-        if (j0 + j < n) v[j] = kv_src[(src0 + f) * 16 + ch];
-      }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int d = __shfl_sync(~0u, to, j0 + j);
-        if (j0 + j < n) kv_dst[(dst0 + d) * 16 + ch] = v[j];
-      }
-    }
+  const int n_rows = kv_apart ? (leaves ? keep : -keep) : n_moves;
+  if (p.apart) {
+    if (rank == 0 && tid == 0) p.listed[unit] = n_rows;
+  } else {
+    move_rows(p, unit, n_rows, rank * kWarps + warp, n_blocks * kWarps);
   }
+}
+
+__global__ void __launch_bounds__(kMoveThreads)
+    move_kernel(const __grid_constant__ EvictParams p, int parts) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int unit = blockIdx.x / parts, part = blockIdx.x - unit * parts;
+  constexpr int kPerBlock = kMoveThreads / 32;
+  move_rows(p, unit, p.listed[unit], part * kPerBlock + (threadIdx.x >> 5), parts * kPerBlock);
 }
 
 }  // namespace
@@ -436,7 +467,7 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const __grid_constant__
 size_t token_evict_bytes(const ri_token_cache& c, int budget) {
   const size_t units = (size_t)c.batch * c.num_kv_heads;
   const size_t W = budget < c.capacity ? budget : c.capacity;
-  return align_up(kStatusBytesHost + 2 * units * W * sizeof(int32_t), 256);
+  return align_up(kStatusBytesHost + (2 * units * W + units) * sizeof(int32_t), 256);
 }
 
 cudaError_t launch_token_evict(const TokenEvictArgs& a, cudaStream_t s) {
@@ -451,6 +482,7 @@ cudaError_t launch_token_evict(const TokenEvictArgs& a, cudaStream_t s) {
   const int cap = a.c.capacity, W = a.budget < cap ? a.budget : cap;
   p.holes = reinterpret_cast<int32_t*>(a.ws + kStatusBytesHost);
   p.moved = p.holes + (size_t)units * W;
+  p.listed = p.moved + (size_t)units * W;
   // Blocks per unit: more while a block has over kRowsPerThread rows per thread
   // and the grid is within a block per SM.
   // (of 8 at most, which any GPC holds twice, unless the slices get too long)
@@ -485,7 +517,22 @@ cudaError_t launch_token_evict(const TokenEvictArgs& a, cudaStream_t s) {
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, p);
+  // Where the clusters leave much of the machine idle (8 heads of a 128K
+  // prompt: 64 blocks), a second launch over all of it moves the rows.
+  p.apart = units * cluster * 4 < 3 * num_sms() && W > kApartRows;
+  e = cudaLaunchKernelEx(&cfg, kernel, p);
+  if (e != cudaSuccess || !p.apart) return e;
+  const int parts = (4 * num_sms() + units - 1) / units;
+  cudaLaunchConfig_t mc = {};
+  mc.gridDim = dim3((unsigned)(units * parts));
+  mc.blockDim = dim3(kMoveThreads);
+  mc.stream = s;
+  cudaLaunchAttribute after[1];
+  after[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  after[0].val.programmaticStreamSerializationAllowed = 1;
+  mc.attrs = after;
+  mc.numAttrs = 1;
+  return cudaLaunchKernelEx(&mc, move_kernel, p, parts);
 }
 
 }  // namespace ri
