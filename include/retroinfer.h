@@ -553,8 +553,8 @@ ri_status ri_gather_shape(int64_t host_copies, int64_t total_copies, int32_t* th
  * pages have no counterpart of these calls. */
 
 /* A strided tensor of heads [B][T][heads][head_dim], head_dim contiguous;
- * strides in elements (any sign of layout: a slice of a projection's output,
- * or the transpose of [B][heads][T][head_dim]). */
+ * strides in elements (a slice of a projection's output, say, or the transpose
+ * of [B][heads][T][head_dim]). */
 typedef struct {
   void* data;
   int64_t stride_b, stride_t, stride_h;
@@ -607,10 +607,10 @@ typedef struct {
  * once to the dtype (RI_BF16, RI_FP16 or RI_FP32) of x and out.
  * x, out   [batch][tokens][heads][head_dim], strided; out may be x itself
  *          (same data and strides), otherwise the two must not overlap.
- *          head_dim 2..256; data aligned to the element.  16-byte aligned
- *          rows with rotary_dim / 2 elements of a multiple of 16 bytes (half
- *          layout; rotary_dim elements when interleaved) take the vector
- *          path, others an element-wise one.
+ *          head_dim 2..256; data aligned to the element.  Rows, halves
+ *          (interleaved: the rotated part) and the rest behind them that all
+ *          start on 16 bytes move 16 bytes at a time, on 4 bytes a word at a
+ *          time, others an element at a time.
  * pos      int32 [batch][tokens], tokens contiguous, pos_stride elements
  *          between sequences (0: one row for all); any value, negative ones
  *          turn backwards.

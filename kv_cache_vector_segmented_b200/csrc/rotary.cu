@@ -29,8 +29,8 @@ constexpr int kBatch = 4;  // rows of copies a thread issues at a time, one batc
 // Cosine and sine of pos * turns / 2^64 turns, times magnitude.  The fraction's
 // top two bits (after adding an eighth) are the quadrant, the rest an angle x
 // of at most pi / 4: sin x = x + x^3 p(x^2), cos x = 1 - x^2 / 2 + x^4 q(x^2)
-// with p, q interpolated at Chebyshev nodes (off by 8.1e-9 and 5.9e-10).
-// About 25 instructions; sincospif took about 185 and was the bound.
+// with p, q interpolated at Chebyshev nodes (off by 8.1e-9 and 5.9e-10).  The
+// fraction needs no range reduction, which a call for any angle begins with.
 __device__ __forceinline__ void turn_angle(unsigned long long turns, int pos, float magnitude,
                                            float* c, float* s) {
   const uint32_t t = static_cast<uint32_t>(
@@ -78,41 +78,48 @@ __device__ __forceinline__ float from_f<float>(float v) {
   return v;
 }
 
-// ------------------------------------------------------- 16 bytes at a time
-// V = 16 / sizeof(T) elements of an access, as floats and back.
-template <typename T>
-__device__ __forceinline__ void unpack(const uint4& v, float (&f)[16 / sizeof(T)]) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+// ------------------------------------------------- words of 2 x 16 or 32 bits
+// An access moves N = 4 words (16 bytes) or one; its V elements as floats and
+// back.
+template <int N>
+struct alignas(4 * N) Words {
+  uint32_t w[N];
+};
+template <typename T, int N>
+__device__ __forceinline__ void unpack(const Words<N>& x, float (&f)[4 * N / sizeof(T)]) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < N; ++i) {
     if constexpr (sizeof(T) == 4) {
-      f[i] = __uint_as_float(w[i]);
+      f[i] = __uint_as_float(x.w[i]);
     } else if constexpr (std::is_same<T, __half>::value) {
-      const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-      f[2 * i] = x.x;
-      f[2 * i + 1] = x.y;
+      const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&x.w[i]));
+      f[2 * i] = v.x;
+      f[2 * i + 1] = v.y;
     } else {
-      f[2 * i] = __uint_as_float(w[i] << 16);
-      f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+      f[2 * i] = __uint_as_float(x.w[i] << 16);
+      f[2 * i + 1] = __uint_as_float(x.w[i] & 0xFFFF0000u);
     }
   }
 }
-template <typename T>
-__device__ __forceinline__ uint4 pack(const float (&f)[16 / sizeof(T)]) {
-  uint32_t w[4];
+template <typename T, int N>
+__device__ __forceinline__ void pack(const float (&f)[4 * N / sizeof(T)], Words<N>* x) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < N; ++i) {
     if constexpr (sizeof(T) == 4) {
-      w[i] = __float_as_uint(f[i]);
+      x->w[i] = __float_as_uint(f[i]);
     } else if constexpr (std::is_same<T, __half>::value) {
       const __half2 h = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
-      w[i] = *reinterpret_cast<const uint32_t*>(&h);
+      x->w[i] = *reinterpret_cast<const uint32_t*>(&h);
     } else {
       const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
-      w[i] = *reinterpret_cast<const uint32_t*>(&h);
+      x->w[i] = *reinterpret_cast<const uint32_t*>(&h);
     }
   }
-  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+template <int N>
+__device__ __forceinline__ void copy_async(Words<N>* smem, const void* g) {
+  if constexpr (N == 4) cp_async16(smem, g);
+  else cp_async4(smem, g);
 }
 
 // The rows (heads) of a token, in the order the kernels take them, and where
@@ -181,7 +188,7 @@ struct StepRows {  // ri_token_append: the query heads, the keys, the values
   }
 };
 
-// A block's 256 threads: `lanes` accesses ("items") of a row, fastest, so that
+// A block's 256 threads: `lanes` accesses of V elements ("items") of a row, fastest, so that
 // a row is one contiguous piece; then `row_slots` rows; then tokens.  Items:
 //  half layout  item i turns elements [i V, +V) with those n further on;
 //  interleaved  item i turns the pairs inside elements [i V, +V);
@@ -217,16 +224,17 @@ Shape shape_of(int turned, int items, long long tokens, int rows) {
 // angles are computed once per thread, for all its rows.  Measured: 128K
 // tokens of 8 heads 93-95 us (5.7 TB/s), one row of copies at a time 104 us,
 // rows held in registers behind a block's shared table of angles 96-104 us.
-template <typename T, bool INTER, class Rows>
+template <typename T, int N, bool INTER, class Rows>
 __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     rows_kernel(const __grid_constant__ Rows rows, const ri_rope rope,
                 const int32_t* __restrict__ pos, long long pos_stride, int T_, unsigned tokens,
                 float sign, const Shape sh) {
-  constexpr int V = 16 / (int)sizeof(T);
+  constexpr int V = 4 * N / (int)sizeof(T);
+  static_assert(!INTER || V > 1, "an access holds whole pairs");
   constexpr int kRaws = INTER ? 1 : 2, kPairs = INTER ? V / 2 : V;
-  extern __shared__ uint4 ring_[];  // [2 kBatch][kRaws][kThreads]
-  auto ring = [&](int stage, int raw) -> uint4& {
-    return ring_[(stage * kRaws + raw) * kThreads + threadIdx.x];
+  extern __shared__ uint4 ring_[];  // [2 kBatch][kRaws][kThreads] accesses
+  auto ring = [&](int stage, int raw) -> Words<N>& {
+    return reinterpret_cast<Words<N>*>(ring_)[(stage * kRaws + raw) * kThreads + threadIdx.x];
   };
   const int lane = threadIdx.x & (sh.lanes - 1), slot = threadIdx.x / sh.lanes;
   const int token_slots = kThreads / sh.lanes / sh.row_slots;
@@ -248,8 +256,8 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     for (int j = 0; j < kBatch; ++j)
       if (ki < tokens) {
         const T* src = rows.from(bi, ti, ri) + at;
-        cp_async16(&ring(first + j, 0), src);
-        if (kRaws == 2 && turns) cp_async16(&ring(first + j, kRaws - 1), src + n);
+        copy_async(&ring(first + j, 0), src);
+        if (kRaws == 2 && turns) copy_async(&ring(first + j, kRaws - 1), src + n);
         ri += sh.row_slots;
         if (ri >= n_rows) {
           ri = r0;
@@ -286,9 +294,9 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
         cp_async_wait<1>();
       }
       T* dst = rows.to(b, t, r, lane == 0);
-      uint4 x = ring(stage, 0);
+      Words<N> x = ring(stage, 0);
       if (!turns) {
-        if (dst) *reinterpret_cast<uint4*>(dst + at) = x;
+        if (dst) *reinterpret_cast<Words<N>*>(dst + at) = x;
       } else if constexpr (INTER) {
         if (rows.turned(r)) {
           float f[V];
@@ -299,11 +307,11 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
             f[2 * i] = u * c[i] - v * s[i];
             f[2 * i + 1] = v * c[i] + u * s[i];
           }
-          x = pack<T>(f);
+          pack<T>(f, &x);
         }
-        if (dst) *reinterpret_cast<uint4*>(dst + at) = x;
+        if (dst) *reinterpret_cast<Words<N>*>(dst + at) = x;
       } else {
-        uint4 y = ring(stage, kRaws - 1);
+        Words<N> y = ring(stage, kRaws - 1);
         if (rows.turned(r)) {
           float u[V], v[V];
           unpack<T>(x, u);
@@ -314,12 +322,12 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
             u[i] = w * c[i] - v[i] * s[i];
             v[i] = v[i] * c[i] + w * s[i];
           }
-          x = pack<T>(u);
-          y = pack<T>(v);
+          pack<T>(u, &x);
+          pack<T>(v, &y);
         }
         if (dst) {
-          *reinterpret_cast<uint4*>(dst + at) = x;
-          *reinterpret_cast<uint4*>(dst + at + n) = y;
+          *reinterpret_cast<Words<N>*>(dst + at) = x;
+          *reinterpret_cast<Words<N>*>(dst + at + n) = y;
         }
       }
       stage = (stage + 1) % (2 * kBatch);
@@ -338,8 +346,8 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
 }
 
 // ------------------------------------------------ any strides and alignment
-// One thread per (token, row group, element or pair): heads whose rows do not
-// start on 16 bytes, or whose halves do not.
+// One thread per element or pair: 16-bit heads whose rows or halves do not
+// start on a word, interleaved fp32 ones that do not start on 16 bytes.
 template <typename T, class Rows>
 __global__ void __launch_bounds__(kThreads)
     rows_any_kernel(const __grid_constant__ Rows rows, const ri_rope rope,
@@ -385,54 +393,69 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
-// `vec`: every row and both halves start on 16 bytes.  `rest`: the elements
-// behind the turned ones are copied too.  `slot`: of the kernel in set_smem_once's table.
-template <typename T, class Rows>
-cudaError_t launch_rows(const Rows& rows, const ri_rope& rope, const int32_t* pos,
-                        long long pos_stride, int T_, int B, int d, bool inverse, bool vec,
-                        bool rest, int slot, cudaStream_t st) {
-  constexpr int V = 16 / (int)sizeof(T);
-  const unsigned tokens = (unsigned)B * T_;  // at most 2^31 (checked by the calls)
-  const float sign = inverse ? -1.f : 1.f;
-  const int rd = rope.rotary_dim;
-  if (!vec) {
-    const int items = rd / 2 + (rest ? d - rd : 0);
-    const unsigned fill = 8u * num_sms();
-    rows_any_kernel<T, Rows><<<(unsigned)(tokens < fill ? tokens : fill), kThreads, 0, st>>>(
-        rows, rope, pos, pos_stride, T_, tokens, sign, d, items);
-  } else {
-    const int turned = rope.interleaved ? rd / V : rd / 2 / V;
-    const int items = turned + (rest ? (d - rd) / V : 0);
-    const Shape sh = shape_of(turned, items, tokens, rows.count());
-    const size_t ring = 2 * kBatch * kThreads * sizeof(uint4);  // per access of a row
-    if (rope.interleaved) {
-      rows_kernel<T, true, Rows><<<sh.blocks, kThreads, ring, st>>>(rows, rope, pos, pos_stride,
-                                                                    T_, tokens, sign, sh);
-    } else {
-      const cudaError_t e = set_smem_once(
-          slot, reinterpret_cast<const void*>(rows_kernel<T, false, Rows>), (int)(2 * ring));
-      if (e != cudaSuccess) return e;
-      rows_kernel<T, false, Rows><<<sh.blocks, kThreads, 2 * ring, st>>>(
-          rows, rope, pos, pos_stride, T_, tokens, sign, sh);
-    }
+// The widest access, in bytes, that every row, the second half's start and the
+// rest's start allow: 16, 4, or less (0).
+int width_of(const ri_rope& rope, int d, int size, const ri_heads* heads, int count) {
+  unsigned long long bits = (unsigned)(rope.interleaved ? rope.rotary_dim : rope.rotary_dim / 2) *
+                            size;
+  bits |= (unsigned)(rope.rotary_dim * size) | (unsigned)(d * size);
+  for (int i = 0; i < count; ++i)
+    bits |= reinterpret_cast<uintptr_t>(heads[i].data) | (heads[i].stride_b * size) |
+            (heads[i].stride_t * size) | (heads[i].stride_h * size);
+  return bits % 16 == 0 ? 16 : bits % 4 == 0 ? 4 : 0;
+}
+
+struct RowsCall {
+  ri_rope rope;
+  const int32_t* pos;
+  long long pos_stride;
+  int T, B, d;
+  bool inverse;
+  bool rest;  // the elements behind the turned ones are copied too
+  int slot;   // of the 16-byte kernel in set_smem_once's table
+};
+
+template <typename T, int N, bool INTER, class Rows>
+cudaError_t launch_words(const Rows& rows, const RowsCall& c, cudaStream_t st) {
+  constexpr int V = 4 * N / (int)sizeof(T);
+  const int rd = c.rope.rotary_dim;
+  const int turned = INTER ? rd / V : rd / 2 / V;
+  const int items = turned + (c.rest ? (c.d - rd) / V : 0);
+  const unsigned tokens = (unsigned)c.B * c.T;  // below 2^31 (checked by the calls)
+  const Shape sh = shape_of(turned, items, tokens, rows.count());
+  constexpr size_t ring = 2 * kBatch * (INTER ? 1 : 2) * kThreads * sizeof(Words<N>);
+  auto kernel = rows_kernel<T, N, INTER, Rows>;
+  if (ring > 48 << 10) {
+    const cudaError_t e = set_smem_once(c.slot, reinterpret_cast<const void*>(kernel), (int)ring);
+    if (e != cudaSuccess) return e;
   }
+  kernel<<<sh.blocks, kThreads, ring, st>>>(rows, c.rope, c.pos, c.pos_stride, c.T, tokens,
+                                            c.inverse ? -1.f : 1.f, sh);
   return cudaGetLastError();
 }
 
-bool vec_ok(const ri_heads& x, int size) {
-  return aligned16(x.data) && x.stride_b * size % 16 == 0 && x.stride_t * size % 16 == 0 &&
-         x.stride_h * size % 16 == 0;
+template <typename T, class Rows>
+cudaError_t launch_rows(const Rows& rows, const RowsCall& c, int width, cudaStream_t st) {
+  const bool inter = c.rope.interleaved;
+  if (width == 16)
+    return inter ? launch_words<T, 4, true>(rows, c, st) : launch_words<T, 4, false>(rows, c, st);
+  if (width == 4 && !inter) return launch_words<T, 1, false>(rows, c, st);
+  if constexpr (sizeof(T) == 2)  // (a word of fp32 holds no pair)
+    if (width == 4) return launch_words<T, 1, true>(rows, c, st);
+  const unsigned tokens = (unsigned)c.B * c.T, fill = 8u * num_sms();
+  const int rd = c.rope.rotary_dim, items = rd / 2 + (c.rest ? c.d - rd : 0);
+  rows_any_kernel<T, Rows><<<tokens < fill ? tokens : fill, kThreads, 0, st>>>(
+      rows, c.rope, c.pos, c.pos_stride, c.T, tokens, c.inverse ? -1.f : 1.f, c.d, items);
+  return cudaGetLastError();
 }
 
 template <typename T>
 cudaError_t rotary_of(const RotaryArgs& a, int slot, cudaStream_t s) {
-  constexpr int V = 16 / (int)sizeof(T);
-  const int rd = a.rope.rotary_dim;
-  const bool vec = (a.rope.interleaved ? rd : rd / 2) % V == 0 && a.d % V == 0 && rd % V == 0 &&
-                   vec_ok(a.x, sizeof(T)) && vec_ok(a.out, sizeof(T));
+  const ri_heads both[2] = {a.x, a.out};
   // in place the rest of the head stays where it is
-  return launch_rows<T>(HeadRows<T>{a}, a.rope, a.pos, a.pos_stride, a.T, a.B, a.d, a.inverse,
-                        vec, a.x.data != a.out.data, slot, s);
+  const RowsCall c{a.rope, a.pos, a.pos_stride, a.T, a.B, a.d, a.inverse, a.x.data != a.out.data,
+                   slot};
+  return launch_rows<T>(HeadRows<T>{a}, c, width_of(a.rope, a.d, sizeof(T), both, 2), s);
 }
 
 // The lengths after the call, once every token of it is stored.
@@ -454,11 +477,12 @@ cudaError_t launch_rotary(const RotaryArgs& a, int dtype, cudaStream_t s) {
 cudaError_t launch_token_append(const AppendTokensArgs& a, cudaStream_t s) {
   ri_rope rope = a.rope;
   if (!rope.turns) rope = ri_rope{nullptr, 0, 0, 1.f};  // nothing turns, all is copied
-  const int n = rope.rotary_dim, H = a.c.num_kv_heads;
+  const int H = a.c.num_kv_heads;
   const StepRows rows{a, a.q.data ? H * a.c.group_size : 0, a.lens_out != a.c.lens};
-  const bool vec = (rope.interleaved ? n : n / 2) % 8 == 0 && n % 8 == 0;
-  cudaError_t e = launch_rows<__nv_bfloat16>(rows, rope, a.pos, a.pos_stride, a.T, a.c.batch,
-                                             kHeadDim, false, vec, true, 11, s);
+  const ri_heads given[3] = {a.k, a.v, a.q.data ? a.q : a.k};
+  const RowsCall c{rope, a.pos, a.pos_stride, a.T, a.c.batch, kHeadDim, false, true, 11};
+  const cudaError_t e =
+      launch_rows<__nv_bfloat16>(rows, c, width_of(rope, kHeadDim, 2, given, 3), s);
   if (e != cudaSuccess || rows.apart || rows.at_end()) return e;
   const int units = a.c.batch * H;
   advance_kernel<<<(units + 255) / 256, 256, 0, s>>>(rows, units);

@@ -89,7 +89,7 @@ def test_rotary_strides(R, interleaved):
     t = R.RotaryTable.make(64, interleaved=interleaved, device=DEV)
     f, mag = T.frequencies(64, 10000.0)
     pos = torch.arange(Tn, dtype=torch.int32).expand(B, Tn)
-    for pad in (0, 8, 3):
+    for pad in (0, 8, 2, 3):
         big = torch.randn(B, Tn, 3 * H, d + pad, generator=_gen(pad)).bfloat16().to(DEV)
         x = big[:, :, H:2 * H, :d]
         before = big.clone()
