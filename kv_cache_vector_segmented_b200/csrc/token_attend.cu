@@ -448,12 +448,14 @@ __device__ __forceinline__ void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64
       : "memory");
 }
 
-__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, int x, int y, int z,
-                                            uint64_t* bar) {
+// One K or V tile: 128 tokens from token `y` on, as two halves of 64 columns.
+__device__ __forceinline__ void tma_load_tile(void* dst, const CUtensorMap* map, int y, int head,
+                                              uint64_t* bar) {
   asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(y), "r"(0), "r"(head),
+      "r"(smem_u32(bar))
       : "memory");
 }
 
@@ -572,8 +574,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
           if (!ok) return;
           uint8_t* dst = ring + st * kTileBytes;
           mbar_arrive_expect_tx(&sh->full[st], kTileBytes);
-          tma_load_3d(dst, map, 0, t * kTile, head, &sh->full[st]);
-          tma_load_3d(dst + kHalfTile, map, 64, t * kTile, head, &sh->full[st]);
+          tma_load_tile(dst, map, t * kTile, head, &sh->full[st]);
           ++n;
         };
         for (int u = u0; u < plan.units && plan.start(u) < x1; ++u) {
@@ -1144,17 +1145,18 @@ EncodeTiledFn encode_fn() {
   return fn;
 }
 
-// [heads][length][128] bf16 with the prefix's strides, boxes of 128 tokens x
-// 64 columns (128-byte swizzle); rows past the length read as zero.
+// [heads][length][128] bf16 with the prefix's strides, seen as [heads][2][length]
+// [64]: a box is 128 tokens of both halves, each half 128-byte swizzled; rows
+// past the length read as zero.
 cudaError_t encode_prefix(CUtensorMap* map, const void* base, const ri_token_prefix& p,
                           int heads) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return cudaErrorNotSupported;
-  cuuint64_t dims[3] = {(cuuint64_t)kD, (cuuint64_t)p.length, (cuuint64_t)heads};
-  cuuint64_t strides[2] = {(cuuint64_t)p.stride_t * 2, (cuuint64_t)p.stride_h * 2};
-  cuuint32_t box[3] = {64, kTile, 1};
-  cuuint32_t estr[3] = {1, 1, 1};
-  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box,
+  cuuint64_t dims[4] = {64, (cuuint64_t)p.length, 2, (cuuint64_t)heads};
+  cuuint64_t strides[3] = {(cuuint64_t)p.stride_t * 2, 128, (cuuint64_t)p.stride_h * 2};
+  cuuint32_t box[4] = {64, kTile, 2, 1};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box,
             estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
