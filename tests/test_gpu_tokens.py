@@ -369,6 +369,13 @@ def test_attend_long(R):
     _attend_case(R, 2, 2, 7, 40000, 100, _ragged(2, 2, 100))
 
 
+def test_attend_long_and_mixed_tiles(R):
+    """Three row tiles (a pair and a single one) over many key tiles, the blocks'
+    shares cut at odd places."""
+    _attend_case(R, 65, 1, 4, 20011, 40, _ragged(65, 1, 40))
+    _attend_case(R, 37, 3, 8, 9001, 40, _ragged(37, 3, 40))
+
+
 def test_attend_bad_lengths_reported(R):
     c = _random_cache(R, 2, 2, 4, 30, [0] * 4, 1, poison=False)
     c.lens.copy_(torch.tensor([[-3, 31], [2 ** 31 - 1, 4]], dtype=torch.int32))
@@ -481,6 +488,13 @@ def test_evict_ties_and_odd_values(R, edit, into):
 def test_evict_long(R):
     _evict_case(R, 1, 2, 70000, [70000, 65000], 5000, 4, 64, "other")
     _evict_case(R, 1, 1, 40000, [40000], 39000, 4, 64, "self")
+
+
+@pytest.mark.parametrize("into", ["self", "shared", "other"])
+def test_evict_few_heads(R, into):
+    """Few heads with many rows: the rows move in a launch of their own."""
+    _evict_case(R, 1, 2, 9000, [9000, 4000], 4500, 4, 64, into)
+    _evict_case(R, 1, 1, 9000, [4100], 4500, 4, 64, into)
 
 
 @pytest.mark.parametrize("into", ["self", "shared", "other"])
@@ -629,3 +643,66 @@ def test_captured_steps_share_a_workspace(R):
             assert _same(a, b)
         for a, b in zip(x[3], y[3]):
             assert torch.equal(a, b)
+
+
+def test_side_stream_equals_default(R):
+    """The decode loop on a stream of its own: the same results, bit for bit."""
+    B, H, G, P = 2, 2, 4, 200
+    t = R.RotaryTable.make(128, device=DEV)
+    prefix = _prefix(H, P, 6, "dense")
+
+    def loop():
+        c = R.TokenCache.empty(B, H, G, 24, DEV)
+        c.K.zero_()
+        c.V.zero_()
+        got = [(out.clone(), lse.clone()) for _, _, out, lse, _ in
+               _steps(R, c, t, prefix, P, 20, 10)]
+        return got, _state(c)
+
+    want, state = loop()
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream(DEV)
+    with torch.cuda.stream(s):
+        got, state2 = loop()
+    s.synchronize()
+    for a, b in zip(want, got):
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    assert all(_same(state[k], state2[k]) for k in state)
+
+
+def test_captured_long_calls(R):
+    """A graph of the calls at sizes that take all their launches (prefix, own
+    tokens, merge; selection and moves): replays repeat the eager results."""
+    B, H, G, P, cap, budget = 1, 2, 4, 5000, 9000, 4200
+    c = _random_cache(R, B, H, G, cap, [8800, 9000], 3)
+    prefix = _prefix(H, P, 3, "dense")
+    q = torch.randn(B, H * G, 128, generator=_gen(8)).bfloat16().to(DEV)
+    out = R.TokenCache(c.K, c.V, *(torch.zeros_like(x) for x in (c.pos, c.weight, c.lens)), G)
+    ws = R.alloc_workspace(max(R.token_attend_workspace_bytes(c, P),
+                               R.token_evict_workspace_bytes(c, budget)), DEV)
+    o, l = torch.empty_like(q), torch.empty(B, H * G, device=DEV)
+    before = _state(c)
+
+    def calls():
+        R.token_attend(q, c, prefix, out=o, lse=l, workspace=ws)
+        R.token_evict(c, budget, 0, 64, out=out, workspace=ws)
+
+    def restore():
+        c.K.copy_(before["K"])
+        c.V.copy_(before["V"])
+        c.weight.copy_(before["weight"])
+
+    calls()
+    want = (o.clone(), l.clone(), _state(out))
+    restore()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        calls()
+    for _ in range(3):
+        restore()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(o, want[0]) and torch.equal(l, want[1])
+        assert all(_same(getattr(out, k), v) for k, v in want[2].items())
+    assert R.read_device_status(ws) == 0

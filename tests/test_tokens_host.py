@@ -134,6 +134,15 @@ def test_size_limits(R, C):
     assert lib.ri_token_attend_workspace(b(_cache(C, batch=65537, num_kv_heads=1)), 0) == 0
     assert lib.ri_token_attend_workspace(b(_cache(C, capacity=(1 << 28) + 1)), 0) == 0
     assert lib.ri_token_attend_workspace(b(_cache(C)), -1) == 0
+    many = _cache(C, batch=8192, num_kv_heads=8, group_size=8)  # over 2^31 tiles of work
+    assert lib.ri_token_attend_workspace(b(many), 1 << 28) == 0
+    p = C.CTokenPrefix(PTR, PTR, 1 << 28, 0, 128, 1 << 35)
+    assert lib.ri_token_attend(b(many), PTR, b(p), PTR, None, 1, PTR, 1 << 40, None) == UNSUPPORTED
+    x, rope = C.CHeads(PTR, 512, 256, 128), C.CRope(PTR, 128, 0, 1.0)
+    assert lib.ri_rotary(1 << 16, 1 << 15, 1, 128, 0, b(x), PTR, 0, b(rope), b(x), 0,
+                         None) == UNSUPPORTED
+    assert lib.ri_token_append(b(_cache(C, batch=32768)), 1 << 16, b(x), b(x), PTR, 0, None, None,
+                               None, 5 * PTR, PTR, None) == UNSUPPORTED
     assert lib.ri_token_evict_workspace(b(_cache(C)), 0) == 0
     big = _cache(C, capacity=(1 << 24) + 1)
     assert lib.ri_token_evict_workspace(b(big), 8) == 0
