@@ -104,12 +104,24 @@ struct AttendLayout {
 AttendLayout layout(const ri_token_cache& c, const PrefixPlan& pp) {
   AttendLayout L;
   const size_t units = (size_t)c.batch * c.num_kv_heads;
-  // own shares: about 16 per SM in all (two rounds of 8 warps), of 64 tokens
-  // or more of a full cache
-  long long splits = (16 * num_sms() + (long long)units - 1) / (long long)units;
-  const long long most = (c.capacity + 63) / 64;
+  // own shares: tasks for 8 warps per SM, two rounds of them, of 64 tokens or
+  // more of a full cache; without a prefix (beside which the rounds run into
+  // one another) up to four, the count whose last round is fullest: 512 heads
+  // of 1.7K tokens 90 us against 94 us
+  const long long warps = 8ll * num_sms(), n = (long long)units;
+  long long most = (c.capacity + 63) / 64;
+  if (most > kMaxSplits) most = kMaxSplits;
+  long long splits = (2 * warps + n - 1) / n;
   if (splits > most) splits = most;
-  if (splits > kMaxSplits) splits = kMaxSplits;
+  double best = 0.0;
+  for (long long s = splits, end = (4 * warps + n - 1) / n; s <= end && s <= most && !pp.blocks; ++s) {
+    const long long rounds = (n * s + warps - 1) / warps;
+    const double full = (double)(n * s) / (double)(rounds * warps);
+    if (full > best + 0.02) {
+      best = full;
+      splits = s;
+    }
+  }
   L.splits = (int)splits;
   const size_t slots = pp.blocks ? 2 * (size_t)(pp.blocks + pp.units) : 0;
   size_t off = kStatusBytesHost;
@@ -391,8 +403,16 @@ __global__ void __launch_bounds__(kOwnThreads)
   if (p.plan.blocks) {
     for (int t = take_task(p); t < p.tasks; t = take_task(p)) own_task<kOwnStages>(p, t, buf);
   } else {
-    for (int t = blockIdx.x * kOwnWarps + warp; t < p.tasks; t += gridDim.x * kOwnWarps)
+    // the first tasks are the warps' own numbers; the next one is asked for
+    // before a task and needed after it
+    const int first = gridDim.x * kOwnWarps;
+    int t = blockIdx.x * kOwnWarps + warp;
+    while (t < p.tasks) {
+      int next = p.tasks;
+      if ((threadIdx.x & 31) == 0 && first < p.tasks) next = first + atomicAdd(p.next_task, 1);
       own_task<kOwnStages>(p, t, buf);
+      t = __shfl_sync(~0u, next, 0);
+    }
   }
   // this launch completes after the prefix launch, so that the merge, which
   // waits for this one, has both
@@ -1238,8 +1258,8 @@ cudaError_t launch_token_attend(const TokenAttendArgs& a, cudaStream_t s) {
     const size_t smem = (size_t)a.c.group_size * (p.plan.blocks + L.splits) * sizeof(float);
     e = launch_dependent(merge_kernel, units * chunks, kMergeThreads, smem, s, p, chunks);
   }
-  // without its merge a prefix launch leaves the counter standing
-  if (e != cudaSuccess && p.plan.blocks) cudaMemsetAsync(p.next_task, 0, sizeof(int), s);
+  // without its merge a launch leaves the counter standing
+  if (e != cudaSuccess) cudaMemsetAsync(p.next_task, 0, sizeof(int), s);
   return e;
 }
 
