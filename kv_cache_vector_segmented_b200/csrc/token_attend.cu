@@ -10,12 +10,16 @@
 //  merge_kernel   joins the shares by log-sum-exp, writes out and lse, and
 //                 adds the own tokens' probabilities to their weights.
 //
-// Every share is (reference m, sum l, numerator) in units of log2:
-//   l = sum_i 2^(s_i - m),  num = sum_i 2^(s_i - m) v_i,  s = q.k log2(e)/sqrt(d),
-// the merge takes M = max m, l = sum 2^(m - M) l, num likewise.  Scores, sums
-// and numerators are fp32; only the probabilities enter the value product as
-// bf16 (half a step, 2^-8, relative, against the output's own 2^-8), the sum
-// l is taken of the unrounded ones.
+// Every share is (reference m, sums l and r, numerator) in units of log2, with
+// s = q.k log2(e) / sqrt(d), p_i = 2^(s_i - m) and p'_i = p_i rounded to bf16:
+//   l = sum_i p_i,  r = sum_i p'_i,  num = sum_i p'_i v_i;
+// the merge takes M = max m, l = sum 2^(m - M) l, r and num likewise, and gives
+// out = num / r, lse = M + log2 l.  Scores, sums and numerators are fp32; only
+// the probabilities enter the value product as bf16 (the tensor cores take two
+// bf16 operands).  Dividing by the sum of the rounded ones takes out what they
+// are off by in common: a token that holds nearly all weight gives its value.
+// (Summed for every tile, r cost the prefix kernel 7 %; where no key counts
+// for an eighth of its row, the unrounded sum goes into r instead.)
 #include <string.h>
 
 #include "common.cuh"
@@ -95,8 +99,8 @@ constexpr int kMaxSplits = 512;  // bounds the merge's shared memory (8 x (SMs +
 
 struct AttendLayout {
   int splits;  // shares of a (sequence, KV head)'s own tokens, a warp's work each
-  // prefix shares: ml fp32 [slots][128][2], num fp32 [slots][128 rows][128];
-  // own shares: ml [units][splits][G][2], num [units][splits][G][128];
+  // prefix shares: ml fp32 [slots][128][4] (m, l, r, 0), num fp32 [slots][128
+  // rows][128]; own shares: ml [units][splits][G][4], num [units][splits][G][128];
   // score fp32 [units][capacity][Gp], Gp = 4 or 8
   size_t off_pml, off_pnum, off_ml, off_num, off_score, total;
 };
@@ -126,11 +130,11 @@ AttendLayout layout(const ri_token_cache& c, const PrefixPlan& pp) {
   const size_t slots = pp.blocks ? 2 * (size_t)(pp.blocks + pp.units) : 0;
   size_t off = kStatusBytesHost;
   L.off_pml = off;
-  off = align_up(off + slots * kTile * 2 * sizeof(float), 256);
+  off = align_up(off + slots * kTile * sizeof(float4), 256);
   L.off_pnum = off;
   off = align_up(off + slots * kTile * kD * sizeof(float), 256);
   L.off_ml = off;
-  off = align_up(off + units * splits * c.group_size * 2 * sizeof(float), 256);
+  off = align_up(off + units * splits * c.group_size * sizeof(float4), 256);
   L.off_num = off;
   off = align_up(off + units * splits * c.group_size * kD * sizeof(float), 256);
   L.off_score = off;
@@ -146,9 +150,9 @@ struct AttendParams {
   const __nv_bfloat16* q;
   __nv_bfloat16* out;
   float* lse;
-  float* pml;
+  float4* pml;
   float* pnum;
-  float* ml;
+  float4* ml;
   float* num;
   float* score;
   int* status;
@@ -193,6 +197,10 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
+
+// The two values of a packed pair.
+__device__ __forceinline__ float bf16_lo(uint32_t p) { return __uint_as_float(p << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t p) { return __uint_as_float(p & 0xFFFF0000u); }
 
 // True in one lane of a converged warp, the same one each time.
 __device__ __forceinline__ bool elect_one() {
@@ -267,9 +275,9 @@ __device__ __forceinline__ void own_task(const AttendParams& p, int task, uint32
   const int tiles = (len + kOwnTokens - 1) / kOwnTokens;
   const int t0 = (int)((long long)tiles * split / p.splits);
   const int t1 = (int)((long long)tiles * (split + 1) / p.splits);
-  float* ml = p.ml + ((size_t)unit * p.splits + split) * G * 2;
+  float4* ml = p.ml + ((size_t)unit * p.splits + split) * G;
   if (t0 >= t1) {
-    if (lane < G) *reinterpret_cast<float2*>(ml + lane * 2) = make_float2(-INFINITY, 0.f);
+    if (lane < G) ml[lane] = make_float4(-INFINITY, 0.f, 0.f, 0.f);
     return;
   }
   const uint8_t* K = static_cast<const uint8_t*>(p.c.K) + (size_t)unit * cap * kD * 2;
@@ -304,7 +312,7 @@ __device__ __forceinline__ void own_task(const AttendParams& p, int task, uint32
     qa[k][0] = g < G ? q[k * 8 + tq] : 0u;
     qa[k][1] = g < G ? q[k * 8 + 4 + tq] : 0u;
   }
-  float m = -INFINITY, l = 0.f;  // of query g, over this thread's columns for l
+  float m = -INFINITY, l = 0.f, rs = 0.f;  // of query g, over this thread's columns for l, r
   float o[8][4];                 // numerator^T: rows d = 16 i + lane / 4 (+ 8), columns 2 tq, + 1
 #pragma unroll
   for (int i = 0; i < 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
@@ -345,6 +353,7 @@ __device__ __forceinline__ void own_task(const AttendParams& p, int task, uint32
       const float f = m == -INFINITY ? 0.f : exp2_approx(m - mn);
       m = mn;
       l *= f;
+      rs *= f;
       const float f0 = __shfl_sync(~0u, f, 8 * tq), f1 = __shfl_sync(~0u, f, 8 * tq + 4);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
@@ -358,6 +367,7 @@ __device__ __forceinline__ void own_task(const AttendParams& p, int task, uint32
     for (int i = 0; i < 4; ++i) x[i] = exp2_approx(x[i] - m);
     l += (x[0] + x[1]) + (x[2] + x[3]);
     const uint32_t p0 = pack_bf16(x[0], x[1]), p1 = pack_bf16(x[2], x[3]);
+    rs += (bf16_lo(p0) + bf16_hi(p0)) + (bf16_lo(p1) + bf16_hi(p1));
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       // V^T: matrices keys 0-7 / 8-15 (lane bit 4) x d halves of 16 (bit 3)
@@ -370,7 +380,9 @@ __device__ __forceinline__ void own_task(const AttendParams& p, int task, uint32
   }
   l += __shfl_xor_sync(~0u, l, 1);
   l += __shfl_xor_sync(~0u, l, 2);
-  if (tq == 0 && g < G) *reinterpret_cast<float2*>(ml + g * 2) = make_float2(m, l);
+  rs += __shfl_xor_sync(~0u, rs, 1);
+  rs += __shfl_xor_sync(~0u, rs, 2);
+  if (tq == 0 && g < G) ml[g] = make_float4(m, l, rs, 0.f);
   float* num = p.num + ((size_t)unit * p.splits + split) * G * kD;
 #pragma unroll
   for (int e = 0; e < 2; ++e)
@@ -780,7 +792,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
       const int row_tile0 = s.row0 + (s.pair ? slot * kTile : 0);
       const bool live = row_tile0 + (warp & 3) * 32 < plan.rows;  // any row of this warp
       const int step = s.pair ? 1 : 2;
-      float m = 0.f, l = 0.f;
+      float m = 0.f, l = 0.f, rs = 0.f;
       bool any = false;
       for (int t = s.t0 + (s.pair ? 0 : slot); t < s.t1; t += step) {
         wait(&sh->s_full[slot], s_phase);
@@ -820,6 +832,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
               const float f = exp2_approx(m - mn);
               m = mn;
               l *= f;
+              rs *= f;
               uint32_t o[16];
 #pragma unroll 1
               for (int c = 0; c < 8; ++c) {  // 16 columns: the scores stay in registers
@@ -832,6 +845,11 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
           }
           any = true;
           const f2 scale = make_f2(kScaleLog2, kScaleLog2), shift = make_f2(-m, -m);
+          // The rounded sum is worth its cost where one key may count for much
+          // of a row (an eighth of what it has gathered): there the probabilities
+          // are read back; elsewhere their errors average out and the exact
+          // sum stands in for it.
+          const bool heavy = __any_sync(~0u, exp2_approx(top - m) * 8.f > l);
           f2 sum[2] = {make_f2(0.f, 0.f), make_f2(0.f, 0.f)};
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
@@ -848,17 +866,33 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
               pk[i] = pack_bf16(a, b);
             }
             tmem_st16(t_s + c * 16, pk);
-            if (c & 1) {  // 64 keys are through: their products may start
+            if (c == 1) {  // 64 keys are through: their products may start
               tmem_wait_st();
               tc_fence_before();
               __syncwarp();
-              if (lane == 0) mbar_arrive(&sh->p_full[slot][c >> 1]);
+              if (lane == 0) mbar_arrive(&sh->p_full[slot][0]);
             }
           }
           float s0, s1, s2, s3;
           split(sum[0], &s0, &s1);
           split(sum[1], &s2, &s3);
-          l += (s0 + s1) + (s2 + s3);
+          s0 = (s0 + s1) + (s2 + s3);
+          l += s0;
+          tmem_wait_st();
+          if (heavy) {
+            s0 = 0.f;
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              uint32_t pk[16];
+              tmem_ld16(t_s + c * 16, pk);
+#pragma unroll
+              for (int i = 0; i < 16; ++i) s0 += bf16_lo(pk[i]) + bf16_hi(pk[i]);
+            }
+          }
+          rs += s0;
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh->p_full[slot][1]);
         } else if (lane == 0) {
           mbar_arrive(&sh->p_full[slot][0]);
           mbar_arrive(&sh->p_full[slot][1]);
@@ -878,7 +912,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
       constexpr int kCols = 32 * kQTiles, kChunks = kCols / 4;  // columns at a time
       const size_t out_slot = 2 * ((size_t)blockIdx.x + u) + (s.pair ? slot : 0);
       float* num = p.pnum + out_slot * kTile * kD;
-      float* ml = p.pml + out_slot * kTile * 2;
+      float4* ml = p.pml + out_slot * kTile;
       uint8_t* stage = sq + warp * (32 * kCols * 4);
       const int warp_row = (warp & 3) * 32;
       const int n_rows = min(32, plan.rows - row_tile0 - warp_row);  // <= 0: none live
@@ -899,7 +933,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
         named_barrier(1, kSoftmaxWarps * 32);  // both slots' scores are through
         if (ok && live) {
           tc_fence_after();
-          if (lane < n_rows) *reinterpret_cast<float2*>(ml + row * 2) = make_float2(m, l);
+          if (lane < n_rows) ml[row] = make_float4(m, l, rs, 0.f);
 #pragma unroll 1
           for (int c = 0; c < 4; ++c) {
             uint32_t a[32];
@@ -914,15 +948,16 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
           tc_fence_before();
         }
       } else {
-        // both slots hold the same rows: (m, l) change hands, and each
+        // both slots hold the same rows: (m, l, r) change hands, and each
         // warpgroup joins half of the columns of both numerators
         // (a slot without a tile waits for the other's products, which read
         // the query tile this goes over)
         if (!used) wait(&sh->o_full[0], unit_phase);
-        float2* ex = reinterpret_cast<float2*>(sq);  // [2][128]
-        ex[slot * kTile + row] = used ? make_float2(m, l) : make_float2(-INFINITY, 0.f);
+        float4* ex = reinterpret_cast<float4*>(sq);  // [2][128]
+        ex[slot * kTile + row] =
+            used ? make_float4(m, l, rs, 0.f) : make_float4(-INFINITY, 0.f, 0.f, 0.f);
         named_barrier(1, kSoftmaxWarps * 32);
-        const float2 e0 = ex[row], e1 = ex[kTile + row];
+        const float4 e0 = ex[row], e1 = ex[kTile + row];
         named_barrier(1, kSoftmaxWarps * 32);
         const float M = fmaxf(e0.x, e1.x);
         const float f0 = exp2_approx(e0.x - M), f1 = exp2_approx(e1.x - M);
@@ -930,7 +965,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
         if (ok && live) {
           tc_fence_after();
           if (lane < n_rows && slot == 0)
-            *reinterpret_cast<float2*>(ml + row * 2) = make_float2(M, f0 * e0.y + f1 * e1.y);
+            ml[row] = make_float4(M, f0 * e0.y + f1 * e1.y, f0 * e0.z + f1 * e1.z, 0.f);
           const uint32_t t_num = tmem + lane_addr + kColO + slot * 64;
 #pragma unroll 1
           for (int c = 0; c < 2; ++c) {
@@ -988,7 +1023,7 @@ __device__ __forceinline__ Scores load_scores(const AttendParams& p, size_t row,
 __global__ void __launch_bounds__(kMergeThreads, 4)
     merge_kernel(const __grid_constant__ AttendParams p, int chunks) {
   extern __shared__ float factor[];  // [G][shares]
-  __shared__ float sh_lse[kMaxGroup], sh_l[kMaxGroup];
+  __shared__ float sh_lse[kMaxGroup], sh_r[kMaxGroup];
   __shared__ int sh_n[kMaxGroup], sh_slot[kMaxGroup];  // prefix shares, the first one's slot
   __shared__ float4 sh_part[kMergeThreads / 32][32];
   const int unit = blockIdx.x / chunks, chunk = blockIdx.x - unit * chunks;
@@ -1029,35 +1064,43 @@ __global__ void __launch_bounds__(kMergeThreads, 4)
       slot = 2 * (c0 + u) + (r / kTile & 1);
     }
     float* f = factor + g * shares;
-    float m = -INFINITY, l = 0.f;
+    float m = -INFINITY, l = 0.f, rs = 0.f;
     for (int i = lane; i < n_prefix + p.splits; i += 32) {
-      float2 v = make_float2(-INFINITY, 0.f);
+      float4 v = make_float4(-INFINITY, 0.f, 0.f, 0.f);
       if (i < n_prefix) {
         // (a block on the unit's edge may have no tile of it)
         if (plan.tile_at(u, plan.from(c0 + i)) < plan.tile_at(u, plan.from(c0 + i + 1)))
-          v = *reinterpret_cast<const float2*>(p.pml + ((size_t)(slot + 2 * i) * kTile + row) * 2);
+          v = p.pml[(size_t)(slot + 2 * i) * kTile + row];
       } else {
-        v = *reinterpret_cast<const float2*>(
-            p.ml + (((size_t)unit * p.splits + i - n_prefix) * G + g) * 2);
+        v = p.ml[((size_t)unit * p.splits + i - n_prefix) * G + g];
       }
       f[i] = v.x;
       if (v.x > m) {
-        l = l * exp2_approx(m - v.x) + v.y;
+        const float e = exp2_approx(m - v.x);
+        l = l * e + v.y;
+        rs = rs * e + v.z;
         m = v.x;
       } else if (v.x > -INFINITY) {
-        l += v.y * exp2_approx(v.x - m);
+        const float e = exp2_approx(v.x - m);
+        l += v.y * e;
+        rs += v.z * e;
       }
     }
     float M = m;
 #pragma unroll
     for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(~0u, M, o));
-    l = m > -INFINITY ? l * exp2_approx(m - M) : 0.f;
+    const float e = m > -INFINITY ? exp2_approx(m - M) : 0.f;
+    l *= e;
+    rs *= e;
 #pragma unroll
-    for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(~0u, l, o);
+    for (int o = 16; o; o >>= 1) {
+      l += __shfl_xor_sync(~0u, l, o);
+      rs += __shfl_xor_sync(~0u, rs, o);
+    }
     for (int i = lane; i < n_prefix + p.splits; i += 32)
       f[i] = f[i] > -INFINITY ? exp2_approx(f[i] - M) : 0.f;
     if (lane == 0) {
-      sh_l[g] = l;
+      sh_r[g] = rs;
       sh_lse[g] = l > 0.f ? M + log2f(l) : -INFINITY;
       sh_n[g] = n_prefix;
       sh_slot[g] = slot;
@@ -1114,7 +1157,7 @@ __global__ void __launch_bounds__(kMergeThreads, 4)
         }
     }
     if (g < G && part == 0) {
-      const float l = sh_l[g], inv = l > 0.f ? 1.f / l : 0.f;
+      const float inv = sh_r[g] > 0.f ? 1.f / sh_r[g] : 0.f;
       const size_t row = (size_t)unit * G + g;
       *reinterpret_cast<uint2*>(p.out + row * kD + lane * 4) =
           make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
@@ -1217,9 +1260,9 @@ cudaError_t launch_token_attend(const TokenAttendArgs& a, cudaStream_t s) {
   p.q = static_cast<const __nv_bfloat16*>(a.q);
   p.out = static_cast<__nv_bfloat16*>(a.out);
   p.lse = a.lse;
-  p.pml = reinterpret_cast<float*>(a.ws + L.off_pml);
+  p.pml = reinterpret_cast<float4*>(a.ws + L.off_pml);
   p.pnum = reinterpret_cast<float*>(a.ws + L.off_pnum);
-  p.ml = reinterpret_cast<float*>(a.ws + L.off_ml);
+  p.ml = reinterpret_cast<float4*>(a.ws + L.off_ml);
   p.num = reinterpret_cast<float*>(a.ws + L.off_num);
   p.score = reinterpret_cast<float*>(a.ws + L.off_score);
   p.status = reinterpret_cast<int*>(a.ws);

@@ -11,8 +11,10 @@ Tolerances, per element, from the arithmetic:
  * attention: a score is a sum of 128 products of bf16 values in fp32, off by
    at most 128 * 2^-23 * |q| |k| / sqrt(128) =: e (a truncating accumulator
    counted), so a probability is off by a factor within exp(2 e) and 2^-18 for
-   the exponentials, sums and merges in fp32; its rounding to bf16 for the
-   value product adds 2^-8, and the output's own rounding 2^-8 of the value.
+   the exponentials, sums and merges in fp32; rounded to bf16 it is p (1 + d),
+   |d| <= 2^-8, in the value product and in the sum that divides it, so a weight
+   is p (1 + d) / (1 + mean of d), within 2 * 2^-8 / (1 - 2^-8) of p; the
+   output's own rounding adds 2^-8 of the value.
 """
 import math
 
@@ -254,7 +256,7 @@ def _check_attend(R, c, before, q, prefix, out, lse, add=True, scale=1.0):
                 qn[b, h], axis=1).max() / math.sqrt(128)
             off = math.expm1(2 * e) + 2.0 ** -18
             rows = slice(h * G, (h + 1) * G)
-            tol = (off + 2.0 ** -8) * mean + 2.0 ** -8 * np.abs(want)
+            tol = (off + 2 * 2.0 ** -8 / (1 - 2.0 ** -8)) * mean + 2.0 ** -8 * np.abs(want)
             assert (np.abs(o[b, rows] - want) <= tol * (1 + 2.0 ** -8)).all(), (b, h)
             if n + (0 if pk is None else len(pk)) == 0:
                 assert (l[b, rows] == -np.inf).all() and (o[b, rows] == 0).all()
