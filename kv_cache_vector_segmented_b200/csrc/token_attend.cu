@@ -16,7 +16,7 @@
 // the merge takes M = max m, l = sum 2^(m - M) l, r and num likewise, and gives
 // out = num / r, lse = M + log2 l.  Scores, sums and numerators are fp32; only
 // the probabilities enter the value product as bf16 (the tensor cores take two
-// bf16 operands).  Dividing by the sum of the rounded ones takes out what they
+// bf16 operands; an own token's as a sum of two).  Dividing by the sum of the rounded ones takes out what they
 // are off by in common: a token that holds nearly all weight gives its value.
 // (Summed for every tile, r cost the prefix kernel 7 %; where no key counts
 // for an eighth of its row, the unrounded sum goes into r instead.)
@@ -312,7 +312,7 @@ __device__ __forceinline__ void own_task(const AttendParams& p, int task, uint32
     qa[k][0] = g < G ? q[k * 8 + tq] : 0u;
     qa[k][1] = g < G ? q[k * 8 + 4 + tq] : 0u;
   }
-  float m = -INFINITY, l = 0.f, rs = 0.f;  // of query g, over this thread's columns for l, r
+  float m = -INFINITY, l = 0.f;  // of query g, over this thread's columns for l
   float o[8][4];                 // numerator^T: rows d = 16 i + lane / 4 (+ 8), columns 2 tq, + 1
 #pragma unroll
   for (int i = 0; i < 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
@@ -353,7 +353,6 @@ __device__ __forceinline__ void own_task(const AttendParams& p, int task, uint32
       const float f = m == -INFINITY ? 0.f : exp2_approx(m - mn);
       m = mn;
       l *= f;
-      rs *= f;
       const float f0 = __shfl_sync(~0u, f, 8 * tq), f1 = __shfl_sync(~0u, f, 8 * tq + 4);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
@@ -366,23 +365,25 @@ __device__ __forceinline__ void own_task(const AttendParams& p, int task, uint32
 #pragma unroll
     for (int i = 0; i < 4; ++i) x[i] = exp2_approx(x[i] - m);
     l += (x[0] + x[1]) + (x[2] + x[3]);
+    // the probabilities and what their rounding left, as two products: the
+    // copies are the bound here, not the tensor cores
     const uint32_t p0 = pack_bf16(x[0], x[1]), p1 = pack_bf16(x[2], x[3]);
-    rs += (bf16_lo(p0) + bf16_hi(p0)) + (bf16_lo(p1) + bf16_hi(p1));
+    const uint32_t q0 = pack_bf16(x[0] - bf16_lo(p0), x[1] - bf16_hi(p0));
+    const uint32_t q1 = pack_bf16(x[2] - bf16_lo(p1), x[3] - bf16_hi(p1));
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       // V^T: matrices keys 0-7 / 8-15 (lane bit 4) x d halves of 16 (bit 3)
       uint32_t a[4];
       ldsm_x4_t(a, vb + at((lane & 7) + ((lane >> 4) << 3), 2 * i + ((lane >> 3) & 1)));
       mma16816(o[i], a[0], a[1], a[2], a[3], p0, p1);
+      mma16816(o[i], a[0], a[1], a[2], a[3], q0, q1);
     }
     __syncwarp();
     stage = stage + 1 == kStages ? 0 : stage + 1;
   }
   l += __shfl_xor_sync(~0u, l, 1);
   l += __shfl_xor_sync(~0u, l, 2);
-  rs += __shfl_xor_sync(~0u, rs, 1);
-  rs += __shfl_xor_sync(~0u, rs, 2);
-  if (tq == 0 && g < G) ml[g] = make_float4(m, l, rs, 0.f);
+  if (tq == 0 && g < G) ml[g] = make_float4(m, l, l, 0.f);  // p' = p to 2^-17
   float* num = p.num + ((size_t)unit * p.splits + split) * G * kD;
 #pragma unroll
   for (int e = 0; e < 2; ++e)
