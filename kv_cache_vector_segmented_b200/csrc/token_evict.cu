@@ -28,6 +28,7 @@ constexpr int kThreads = 1024;
 constexpr int kBucketBits = 10;  // 1 << kBucketBits == kThreads
 constexpr int kWarps = kThreads / 32;
 constexpr int kMoveThreads = 256;
+constexpr int kRowsInFlight = 8;
 constexpr int kRowsPerThread = 2;
 // rows per unit from which a launch of its own for the moves pays
 constexpr int kApartRows = 2048;
@@ -125,8 +126,8 @@ __device__ __forceinline__ int warps_before(int count, int* sums, int* all) {
 }
 
 // Row moved[k] -> row holes[k] of a unit, for the rows of one warp of `warps`:
-// up to 32 in a row, their numbers in one load, their K and V eight rows in
-// flight.  Sources of moves lie at or behind keep, destinations before it: no
+// up to 32 in a row, their numbers in one load, their K and V kRowsInFlight
+// rows in flight.  Sources of moves lie at or behind keep, destinations before it: no
 // move reads what another writes.
 __device__ __forceinline__ void move_rows(const EvictParams& p, int unit, int n_rows, int warp,
                                           int warps) {
@@ -143,28 +144,40 @@ __device__ __forceinline__ void move_rows(const EvictParams& p, int unit, int n_
   const uint4* kv_src = reinterpret_cast<const uint4*>(lane < 16 ? p.c.K : p.c.V);
   uint4* kv_dst = reinterpret_cast<uint4*>(lane < 16 ? p.o.K : p.o.V);
   const int run = min(32, (n_rows + warps - 1) / warps);
-  for (int k0 = warp * run; k0 < n_rows; k0 += warps * run) {
-    const int n = min(run, n_rows - k0);
-    int from = 0, to = 0;
+  int k0 = warp * run;
+  auto numbers = [&](int k, int* from, int* to) {  // of row k + lane of the list
+    *from = *to = k + lane;
+    if (list && lane < min(run, n_rows - k)) {
+      *from = moved[k + lane];
+      *to = holes[k + lane];
+    }
+  };
+  int from, to;
+  numbers(k0, &from, &to);
+  while (k0 < n_rows) {
+    const int n = min(run, n_rows - k0), next = k0 + warps * run;
+    int next_from, next_to;
+    numbers(next, &next_from, &next_to);  // on their way meanwhile
     if (lane < n) {
-      from = list ? moved[k0 + lane] : k0 + lane;
-      to = list ? holes[k0 + lane] : k0 + lane;
       if (from != to || pos_apart) p.o.pos[dst0 + to] = pos[from];
       if (from != to || weight_apart) p.o.weight[dst0 + to] = weight[from];
     }
-    for (int j0 = 0; j0 < n; j0 += 8) {
-      uint4 v[8];
+    for (int j0 = 0; j0 < n; j0 += kRowsInFlight) {
+      uint4 v[kRowsInFlight];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int f = __shfl_sync(~0u, from, j0 + j);
-        if (j0 + j < n) v[j] = kv_src[(src0 + f) * 16 + ch];
+      for (int j = 0; j < kRowsInFlight; ++j) {
+        const int f = __shfl_sync(~0u, from, (j0 + j) & 31);
+        if (j0 + j < n) v[j] = __ldcs(kv_src + (src0 + f) * 16 + ch);
       }
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int d = __shfl_sync(~0u, to, j0 + j);
-        if (j0 + j < n) kv_dst[(dst0 + d) * 16 + ch] = v[j];
+      for (int j = 0; j < kRowsInFlight; ++j) {
+        const int d = __shfl_sync(~0u, to, (j0 + j) & 31);
+        if (j0 + j < n) __stcs(kv_dst + (dst0 + d) * 16 + ch, v[j]);
       }
     }
+    from = next_from;
+    to = next_to;
+    k0 = next;
   }
 }
 
