@@ -550,7 +550,16 @@ ri_status ri_gather_shape(int64_t host_copies, int64_t total_copies, int32_t* th
  * keys, the append's and the queries as well), and a cache of exact tokens
  * per (sequence, KV head) which a batch reads together with one shared
  * prefix, and which gives up its least-attended tokens under a budget.  The
- * pages have no counterpart of these calls. */
+ * pages have no counterpart of these calls.
+ *  - Calls whose executions may overlap need a workspace each (and may not
+ *    write the same cache); calls on one stream, and graphs replayed one
+ *    after the other, may share one of the largest size.  No other kind of
+ *    call may have used the workspace's status region in between without
+ *    leaving it zero.
+ *  - Make a first call of each kind on a device before capturing one into a
+ *    CUDA graph (kernel attributes are set then).
+ *  - Kernels here overlap their set-up with the end of the launch before
+ *    them and wait for its completion before their first access. */
 
 /* A strided tensor of heads [B][T][heads][head_dim], head_dim contiguous;
  * strides in elements (a slice of a projection's output, say, or the transpose
