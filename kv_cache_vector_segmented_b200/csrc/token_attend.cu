@@ -407,8 +407,8 @@ __device__ __forceinline__ void own_task(const AttendParams& p, int task, uint32
       }
 }
 
-// Tasks [.., tasks) from the shared counter, one at a time; every task's
-// result is the same whoever takes it.
+// The next task of the shared counter (p.tasks or more: none is left).  A
+// task's result is the same whoever takes it.
 __device__ __forceinline__ int take_task(const AttendParams& p) {
   int t = 0;
   if ((threadIdx.x & 31) == 0) t = atomicAdd(p.next_task, 1);

@@ -98,10 +98,11 @@ __device__ __forceinline__ unsigned long long remote_u64(const unsigned long lon
   return v;
 }
 
-// Lane b's copy of a word of block b of the unit (0 from lane n on), so that
-// all blocks' words arrive in one round trip.
+// Lane b's copy of a word of block b of the unit's n (0 from lane n on), so
+// that all blocks' words arrive in one round trip.
 __device__ __forceinline__ int gather_int(const int* p, int n) {
   const int lane = threadIdx.x & 31;
+  if (n == 1) return lane == 0 ? *p : 0;  // the block's own
   return lane < n ? remote_int(p, lane) : 0;
 }
 
@@ -303,12 +304,17 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const __grid_constant__
         break;
       }
       // thread t sums bucket kBuckets - 1 - t, so that a prefix sum runs from the top
-      int v[kMaxCluster], sum = 0;
+      int sum = 0;
+      if (n_blocks == 1) {
+        sum = x.hist[pass][kBuckets - 1 - tid];
+      } else {
+        int v[kMaxCluster];
 #pragma unroll
-      for (int b = 0; b < kMaxCluster; ++b)
-        v[b] = b < n_blocks ? remote_int(&x.hist[pass][kBuckets - 1 - tid], b) : 0;
+        for (int b = 0; b < kMaxCluster; ++b)
+          v[b] = b < n_blocks ? remote_int(&x.hist[pass][kBuckets - 1 - tid], b) : 0;
 #pragma unroll
-      for (int b = 0; b < kMaxCluster; ++b) sum += v[b];
+        for (int b = 0; b < kMaxCluster; ++b) sum += v[b];
+      }
       int upto = sum;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -341,18 +347,22 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const __grid_constant__
           x.mine[atomicAdd(&x.n_mine, 1)] = (unsigned long long)k << 32 | (uint32_t)~(r0 + i);
       }
       unit_sync(n_blocks);
-      int n = gather_int(&x.n_mine, n_blocks), first = 0;  // lane b: block b's
-      for (int b = 0; b < n_blocks; ++b) {
-        const int nb = __shfl_sync(~0u, n, b);
-        for (int i = tid; i < nb; i += kThreads) x.all[first + i] = remote_u64(&x.mine[i], b);
-        first += nb;
+      const unsigned long long* all = x.mine;
+      if (n_blocks > 1) {
+        int n = gather_int(&x.n_mine, n_blocks), first = 0;  // lane b: block b's
+        for (int b = 0; b < n_blocks; ++b) {
+          const int nb = __shfl_sync(~0u, n, b);
+          for (int i = tid; i < nb; i += kThreads) x.all[first + i] = remote_u64(&x.mine[i], b);
+          first += nb;
+        }
+        __syncthreads();
+        all = x.all;
       }
-      __syncthreads();
       {
-        const unsigned long long me = (tid >> 2) < count ? x.all[tid >> 2] : 0ull;
+        const unsigned long long me = (tid >> 2) < count ? all[tid >> 2] : 0ull;
         int larger = 0;
 #pragma unroll 4
-        for (int j = tid & 3; j < count; j += 4) larger += x.all[j] > me;
+        for (int j = tid & 3; j < count; j += 4) larger += all[j] > me;
         larger += __shfl_xor_sync(~0u, larger, 1);
         larger += __shfl_xor_sync(~0u, larger, 2);
         if ((tid >> 2) < count && (tid & 3) == 0 && larger == need - 1) {
@@ -375,7 +385,8 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const __grid_constant__
       int t = warps_before(n, x.warp_b, &all);
       if (tid == 0) x.ties = all;
       unit_sync(n_blocks);
-      t += __reduce_add_sync(~0u, gather_int(&x.ties, rank));
+      const int before = gather_int(&x.ties, n_blocks);
+      t += __reduce_add_sync(~0u, lane < rank ? before : 0);
       for (int s = 0; s < steps; ++s) {
         const int i = row_in(s);
         const uint32_t m = __ballot_sync(~0u, i < rows && key_of(i) == cut_key);
@@ -473,7 +484,9 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const __grid_constant__
   }
 }
 
-__global__ void __launch_bounds__(kMoveThreads)
+// (One block per SM as the compiler's bound: it then keeps all loads of a batch
+// in flight, 107 registers; with 76 the 128K prompt took 49 us instead of 45.)
+__global__ void __launch_bounds__(kMoveThreads, 1)
     move_kernel(const __grid_constant__ EvictParams p, int parts) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int unit = blockIdx.x / parts, part = blockIdx.x - unit * parts;
