@@ -19,10 +19,10 @@
 // machine idle.
 //
 // Bound: reading 8 bytes per token, and 1 KB of traffic per token that changes
-// its row.  Measured: 128 heads of 8K tokens halved 67 us, of which the moves'
+// its row.  Measured: 128 heads of 8K tokens halved 65 us, of which the moves'
 // 262 MB take about 45 (5.8 TB/s) and the selection, latency after latency, 20;
 // 8 heads of 128K reduced to 8K 45 us (29 of them the selection on 64 SMs); one
-// token out of each of 128 heads 12.3 us.
+// token out of each of 128 heads 11.5 us.
 #include "common.cuh"
 #include "internal.h"
 
