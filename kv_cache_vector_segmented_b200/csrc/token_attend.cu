@@ -457,7 +457,8 @@ constexpr int kPrefixThreads = 384;
 // to 112: 256 x 192 + 128 x 112 = 63488.
 constexpr int kRegsSoftmax = 192, kRegsRest = 112;
 // TMEM columns: scores (and, over them, the probabilities) of slot i, then
-// the numerators
+// the numerators.  A tile's scores go over the probabilities of the slot's tile
+// before: one thread issues both products, and its MMAs run in issue order.
 constexpr uint32_t kColS = 0, kColO = 256;
 
 struct PrefixShared {
