@@ -26,7 +26,7 @@
 // products take 1024 cycles of the one, its exponentials 1024 of the other),
 // under the power limit.  Measured: 64 sequences of 4 query heads behind 128K
 // tokens of 8 heads 206-216 us in all (157 us for the prefix alone at 1965 MHz:
-// 0.9 PFLOP/s; tensor pipe active 50 %, special functions 48 %), 16 behind 32K
+// 0.9 PFLOP/s; tensor pipe active 49 %, special functions 46 %), 16 behind 32K
 // 59-61 us (4.1 TB/s over all three launches; the merge and its start take 10).
 // Not kept: part of the exponentials as polynomials on the FMA pipe (184-204
 // against 177 us for the prefix of the largest case: more instructions, more
