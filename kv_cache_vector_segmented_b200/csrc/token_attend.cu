@@ -16,8 +16,9 @@
 // the merge takes M = max m, l = sum 2^(m - M) l, r and num likewise, and gives
 // out = num / r, lse = M + log2 l.  Scores, sums and numerators are fp32; only
 // the probabilities enter the value product as bf16 (the tensor cores take two
-// bf16 operands; an own token's as a sum of two).  Dividing by the sum of the rounded ones takes out what they
-// are off by in common: a token that holds nearly all weight gives its value.
+// bf16 operands; an own token's as a sum of two).  Dividing by the sum of the
+// rounded ones takes out what they are off by in common: a token that holds
+// nearly all weight gives its value.
 // (Summed for every tile, r cost the prefix kernel 7 %; where no key counts
 // for an eighth of its row, the unrounded sum goes into r instead.)
 //
@@ -45,6 +46,9 @@ constexpr float kScaleLog2 = 0.08838834764831845f * 1.4426950408889634f;  // log
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kD = kHeadDim;
 constexpr float kLazy = 8.f;  // log2: the reference moves when the maximum passes it by this
+// The least reference: of a row that has met scores of -inf only, whose
+// probabilities are then 2^-inf = 0 (and not 2^(-inf + inf), NaN).
+constexpr float kLowest = -3.402823466e38f;
 constexpr int kTile = 128;                  // query rows, keys of a tile
 constexpr int kTileBytes = kTile * kD * 2;  // 32 KB of bf16
 constexpr int kHalfTile = kTileBytes / 2;   // 64 of the 128 columns, 128-byte rows
@@ -324,7 +328,7 @@ __device__ __forceinline__ void own_task(const AttendParams& p, int task, uint32
     qa[k][0] = g < G ? q[k * 8 + tq] : 0u;
     qa[k][1] = g < G ? q[k * 8 + 4 + tq] : 0u;
   }
-  float m = -INFINITY, l = 0.f;  // of query g, over this thread's columns for l
+  float m = kLowest, l = 0.f;  // of query g, over this thread's columns for l
   float o[8][4];                 // numerator^T: rows d = 16 i + lane / 4 (+ 8), columns 2 tq, + 1
 #pragma unroll
   for (int i = 0; i < 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
@@ -358,11 +362,11 @@ __device__ __forceinline__ void own_task(const AttendParams& p, int task, uint32
     }
     float top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
     top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
-    top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));  // finite: a tile has a valid token
+    top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
     const bool grow = top > m + kLazy;
     if (__any_sync(~0u, grow)) {
       const float mn = grow ? top : m;
-      const float f = m == -INFINITY ? 0.f : exp2_approx(m - mn);
+      const float f = exp2_approx(m - mn);
       m = mn;
       l *= f;
       const float f0 = __shfl_sync(~0u, f, 8 * tq), f1 = __shfl_sync(~0u, f, 8 * tq + 4);
@@ -836,7 +840,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
           }
           const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * kScaleLog2;
           if (!any) {
-            m = top;
+            m = fmaxf(top, kLowest);
           } else {
             // the numerator is complete up to the previous tile here: the
             // commit that signalled these scores covers every MMA before it
@@ -1181,7 +1185,8 @@ __global__ void __launch_bounds__(kMergeThreads, 4)
   if (i0 >= end) return;
   float lse[kMaxGroup];
 #pragma unroll
-  for (int g = 0; g < kMaxGroup; ++g) lse[g] = g < G ? sh_lse[g] : 0.f;
+  for (int g = 0; g < kMaxGroup; ++g)  // (-inf: every score is -inf, and adds 2^-inf)
+    lse[g] = g < G && sh_lse[g] != -INFINITY ? sh_lse[g] : 0.f;
   auto added = [&](const Scores& s) {  // (entries from G on were never written)
     float w = exp2_approx(s.a.x - lse[0]);
     if (G > 1) w += exp2_approx(s.a.y - lse[1]);
