@@ -688,7 +688,8 @@ size_t ri_token_attend_workspace(const ri_token_cache* cache, int32_t prefix_len
  * q, out   bf16 [B][H_kv G][128];  lse  optional fp32 [B][H_kv G].
  * prefix   NULL or length 0: none.  A row with nothing to attend to gives
  *          out = 0 and lse = -inf; so does one whose scores are all -inf (a
- *          token of score -inf has weight 0). */
+ *          token of score -inf has weight 0).  A NaN or +inf among its scores
+ *          makes a row NaN: out, lse and the weights it adds to. */
 ri_status ri_token_attend(const ri_token_cache* cache, const void* q,
                           const ri_token_prefix* prefix, void* out, float* lse,
                           int32_t add_weight, void* workspace, size_t workspace_bytes,

@@ -10,6 +10,9 @@
 //  merge_kernel   joins the shares by log-sum-exp, writes out and lse, and
 //                 adds the own tokens' probabilities to their weights.
 //
+// A NaN or +inf among a row's scores makes its sums NaN, and so the row: out,
+// lse and the weights that it adds to.
+//
 // Every share is (reference m, sums l and r, numerator) in units of log2, with
 // s = q.k log2(e) / sqrt(d), p_i = 2^(s_i - m) and p'_i = p_i rounded to bf16:
 //   l = sum_i p_i,  r = sum_i p'_i,  num = sum_i p'_i v_i;
@@ -1119,7 +1122,7 @@ __global__ void __launch_bounds__(kMergeThreads, 4)
       f[i] = f[i] > -INFINITY ? exp2_approx(f[i] - M) : 0.f;
     if (lane == 0) {
       sh_r[g] = rs;
-      sh_lse[g] = l > 0.f ? M + log2f(l) : -INFINITY;
+      sh_lse[g] = l == 0.f ? -INFINITY : M + log2f(l);  // (a sum of NaN: NaN)
       sh_n[g] = n_prefix;
       sh_slot[g] = slot;
     }
@@ -1175,7 +1178,7 @@ __global__ void __launch_bounds__(kMergeThreads, 4)
         }
     }
     if (g < G && part == 0) {
-      const float inv = sh_r[g] > 0.f ? 1.f / sh_r[g] : 0.f;
+      const float inv = sh_r[g] == 0.f ? 0.f : 1.f / sh_r[g];  // (a sum of NaN: NaN)
       const size_t row = (size_t)unit * G + g;
       *reinterpret_cast<uint2*>(p.out + row * kD + lane * 4) =
           make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));

@@ -139,6 +139,22 @@ WHERE = {
 }
 
 
+@pytest.mark.parametrize("where", ["query", "own_key", "own_keys", "prefix_key", "prefix_tiles",
+                                   "prefix_keys", "every_key"])
+def test_attend_nan(R, where):
+    """A NaN in a query or a key makes its rows NaN: out, lse and weights."""
+    for i, shape in enumerate(SHAPES):
+        _case(R, *shape, i, lambda s: WHERE[where](s, NAN))
+
+
+@pytest.mark.parametrize("where", ["query", "own_key", "own_keys", "prefix_key", "prefix_tiles",
+                                   "prefix_keys", "every_key"])
+def test_attend_infinite_score(R, where):
+    """A score of +inf has no finite probability: its row is NaN."""
+    for i, shape in enumerate(SHAPES):
+        _case(R, *shape, i, lambda s: WHERE[where](s, INF))
+
+
 @pytest.mark.parametrize("where", ["own_key", "own_tile", "own_keys", "prefix_first",
                                    "prefix_tiles", "prefix_half", "prefix_keys", "every_key"])
 def test_attend_minus_infinite_score(R, where):
