@@ -217,6 +217,14 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return r;
 }
 
+// Towards zero.
+__device__ __forceinline__ uint32_t pack_bf16_down(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rz.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+constexpr float kLeast = 9.1835496e-41f;  // 2^-133, the least bf16 above 0
+
 // The two values of a packed pair.
 __device__ __forceinline__ float bf16_lo(uint32_t p) { return __uint_as_float(p << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t p) { return __uint_as_float(p & 0xFFFF0000u); }
@@ -385,10 +393,13 @@ __device__ __forceinline__ void own_task(const AttendParams& p, int task, uint32
     for (int i = 0; i < 4; ++i) x[i] = exp2_approx(x[i] - m);
     l += (x[0] + x[1]) + (x[2] + x[3]);
     // the probabilities and what their rounding left, as two products: the
-    // copies are the bound here, not the tensor cores
-    const uint32_t p0 = pack_bf16(x[0], x[1]), p1 = pack_bf16(x[2], x[3]);
-    const uint32_t q0 = pack_bf16(x[0] - bf16_lo(p0), x[1] - bf16_hi(p0));
-    const uint32_t q1 = pack_bf16(x[2] - bf16_lo(p1), x[3] - bf16_hi(p1));
+    // copies are the bound here, not the tensor cores.  Rounded towards zero,
+    // and what is left not below kLeast, so that neither part of a probability
+    // is 0 or negative: both products of an infinite value are that infinity.
+    const uint32_t p0 = pack_bf16_down(x[0], x[1]), p1 = pack_bf16_down(x[2], x[3]);
+    auto left = [](float v, float part) { return fmaxf(v - part, fminf(v, kLeast)); };
+    const uint32_t q0 = pack_bf16(left(x[0], bf16_lo(p0)), left(x[1], bf16_hi(p0)));
+    const uint32_t q1 = pack_bf16(left(x[2], bf16_lo(p1)), left(x[3], bf16_hi(p1)));
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       // V^T: matrices keys 0-7 / 8-15 (lane bit 4) x d halves of 16 (bit 3)
@@ -402,7 +413,7 @@ __device__ __forceinline__ void own_task(const AttendParams& p, int task, uint32
   }
   l += __shfl_xor_sync(~0u, l, 1);
   l += __shfl_xor_sync(~0u, l, 2);
-  if (tq == 0 && g < G) ml[g] = make_float4(m, l, l, 0.f);  // p' = p to 2^-17
+  if (tq == 0 && g < G) ml[g] = make_float4(m, l, l, 0.f);  // p' = p to 2^-15
   float* num = p.num + ((size_t)unit * p.splits + split) * G * kD;
 #pragma unroll
   for (int e = 0; e < 2; ++e)

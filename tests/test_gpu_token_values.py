@@ -161,3 +161,22 @@ def test_attend_minus_infinite_score(R, where):
     """A score of -inf has weight 0, in a first tile, a whole share or everywhere."""
     for i, shape in enumerate(SHAPES):
         _case(R, *shape, i, lambda s: WHERE[where](s, -INF))
+
+
+@pytest.mark.parametrize("value", [NAN, INF, -INF])
+@pytest.mark.parametrize("where", ["own_value", "prefix_value"])
+def test_attend_values(R, where, value):
+    """A value's NaN or infinity reaches its column of the output and no other."""
+    for i, shape in enumerate(SHAPES):
+        _case(R, *shape, i, lambda s: WHERE[where](s, value))
+
+
+@pytest.mark.parametrize("value", [NAN, INF, -INF])
+@pytest.mark.parametrize("where", ["own_value", "prefix_value"])
+def test_attend_values_of_equal_scores(R, where, value):
+    """The same with probabilities that a bf16 holds exactly."""
+    def edit(s):
+        WHERE[where](s, value)
+        s["q"].zero_()
+    for i, shape in enumerate(SHAPES):
+        _case(R, *shape, i, edit)
