@@ -1130,7 +1130,7 @@ __global__ void __launch_bounds__(kMergeThreads, 4)
       rs += __shfl_xor_sync(~0u, rs, o);
     }
     for (int i = lane; i < n_prefix + p.splits; i += 32)
-      f[i] = f[i] > -INFINITY ? exp2_approx(f[i] - M) : 0.f;
+      f[i] = f[i] > -INFINITY ? exp2_approx(f[i] - M) : -1.f;  // -1: nothing was written
     if (lane == 0) {
       sh_r[g] = rs;
       sh_lse[g] = l == 0.f ? -INFINITY : M + log2f(l);  // (a sum of NaN: NaN)
@@ -1160,10 +1160,10 @@ __global__ void __launch_bounds__(kMergeThreads, 4)
 #pragma unroll
         for (int j = 0; j < kFlight; ++j) {
           const int i = f0 + j * per_row;
-          w[j] = i < all ? f[i] : 0.f;
+          w[j] = i < all ? f[i] : -1.f;
           v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-          // factor 0: nothing was written there, or nothing that counts
-          if (w[j] > 0.f)
+          // (read with a factor of 0 too: a numerator of NaN counts all the same)
+          if (!(w[j] < 0.f))
             v[j] = *(i < n ? prefix + (size_t)i * 2 * kTile * (kD / 4)
                            : own + (size_t)(i - n) * G * (kD / 4));
         }

@@ -180,3 +180,18 @@ def test_attend_values_of_equal_scores(R, where, value):
         s["q"].zero_()
     for i, shape in enumerate(SHAPES):
         _case(R, *shape, i, edit)
+
+
+@pytest.mark.parametrize("where", ["own_value", "prefix_value"])
+def test_attend_nan_value_of_no_weight(R, where):
+    """A NaN value counts however small its probability is (0 * NaN is NaN)."""
+    def edit(s):
+        WHERE[where](s, NAN)
+        # far below every other score: the probability is 0 in fp32, in a tile or
+        # a share of its own
+        name = "K" if where == "own_value" else "PK"
+        WHERE["own_tile" if name == "K" else "prefix_tiles"](s, -2000.0)
+        if name == "PK" and s["PV"].shape[1]:
+            s["PV"][:, 0, 7] = NAN
+    for i, shape in enumerate(SHAPES):
+        _case(R, *shape, i, edit)
