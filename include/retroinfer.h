@@ -689,7 +689,9 @@ size_t ri_token_attend_workspace(const ri_token_cache* cache, int32_t prefix_len
  * prefix   NULL or length 0: none.  A row with nothing to attend to gives
  *          out = 0 and lse = -inf; so does one whose scores are all -inf (a
  *          token of score -inf has weight 0).  A NaN or +inf among its scores
- *          makes a row NaN: out, lse and the weights it adds to. */
+ *          makes a row NaN: out, lse and the weights it adds to.
+ * A wait inside a kernel that expires (2 s) is recorded as RI_ERR_TIMEOUT: the
+ * rows it concerns are NaN then, and add nothing to the weights. */
 ri_status ri_token_attend(const ri_token_cache* cache, const void* q,
                           const ri_token_prefix* prefix, void* out, float* lse,
                           int32_t add_weight, void* workspace, size_t workspace_bytes,
@@ -745,6 +747,20 @@ ri_status ri_selftest_decode_timeout(const ri_index_config* cfg, const ri_decode
                                      const void* q, const ri_index* idx, void* out,
                                      void* workspace, size_t workspace_bytes, int32_t hand_off,
                                      uint64_t limit_ns, ri_stream_t stream);
+
+/* Self-test of the waits of ri_token_attend: one call (same arguments; the
+ * prefix is needed) whose first block over the prefix leaves a hand-off undone,
+ * every wait limited to limit_ns nanoseconds (at most 10 s):
+ *   hand_off 1: the copies of its second and later tiles are never issued;
+ *   hand_off 2: its scores are never signalled ready.
+ * RI_ERR_TIMEOUT is recorded, the rows that the block has a share of are NaN in
+ * out and lse and add nothing to the weights, and all else is as
+ * ri_token_attend gives it. */
+ri_status ri_selftest_token_attend_timeout(const ri_token_cache* cache, const void* q,
+                                           const ri_token_prefix* prefix, void* out, float* lse,
+                                           int32_t add_weight, void* workspace,
+                                           size_t workspace_bytes, int32_t hand_off,
+                                           uint64_t limit_ns, ri_stream_t stream);
 
 const char* ri_status_string(ri_status status);
 /* Description of the last error of the calling thread ("" if none). */

@@ -25,7 +25,7 @@ _EXPORTS = (
 _TOKEN_EXPORTS = (
     "ROPE_SCALINGS", "RotaryConfig", "RotaryTable", "TokenCache", "rotary", "token_append",
     "token_attend", "token_attend_workspace_bytes", "token_evict",
-    "token_evict_workspace_bytes")
+    "token_evict_workspace_bytes", "selftest_token_attend_timeout")
 
 __all__ = list(_EXPORTS + _TOKEN_EXPORTS)
 

@@ -68,6 +68,9 @@ lib.ri_token_attend_workspace.argtypes = [_P(CTokenCache), _i32]
 lib.ri_token_attend.restype = ctypes.c_int
 lib.ri_token_attend.argtypes = [_P(CTokenCache), _vp, _P(CTokenPrefix), _vp, _vp, _i32, _vp, _sz,
                                 _vp]
+lib.ri_selftest_token_attend_timeout.restype = ctypes.c_int
+lib.ri_selftest_token_attend_timeout.argtypes = [_P(CTokenCache), _vp, _P(CTokenPrefix), _vp, _vp,
+                                                 _i32, _vp, _sz, _i32, ctypes.c_uint64, _vp]
 lib.ri_token_evict_workspace.restype = _sz
 lib.ri_token_evict_workspace.argtypes = [_P(CTokenCache), _i32]
 lib.ri_token_evict.restype = ctypes.c_int
@@ -293,6 +296,22 @@ def token_attend(q: torch.Tensor, cache: TokenCache, prefix: Optional[tuple] = N
     with 128 contiguous; None: none) and the cache's own tokens, whose
     attention weights are added to cache.weight unless add_weight is False.
     Returns (out bf16 [B][H_q][128], lse fp32 [B][H_q])."""
+    return _attend(q, cache, prefix, add_weight, out, lse, workspace, lib.ri_token_attend,
+                   "ri_token_attend")
+
+
+def selftest_token_attend_timeout(q: torch.Tensor, cache: TokenCache, prefix: tuple,
+                                  workspace: torch.Tensor, hand_off: int, limit_ns: int,
+                                  add_weight: bool = True):
+    """ri_selftest_token_attend_timeout: a call whose first block over the
+    prefix leaves one hand-off undone (1: a tile's copy, 2: the scores'
+    signal), every wait limited to limit_ns."""
+    return _attend(q, cache, prefix, add_weight, None, None, workspace,
+                   lib.ri_selftest_token_attend_timeout, "ri_selftest_token_attend_timeout",
+                   hand_off, limit_ns)
+
+
+def _attend(q, cache, prefix, add_weight, out, lse, workspace, fn, where, *test):
     B, H, d, dev = cache.batch, cache.num_kv_heads, cache.head_dim, cache.device
     shape = (B, H * cache.group_size, d)
     q_ptr = _dense(q, "q", torch.bfloat16, shape, dev)
@@ -329,8 +348,8 @@ def token_attend(q: torch.Tensor, cache: TokenCache, prefix: Optional[tuple] = N
         workspace = alloc_workspace(token_attend_workspace_bytes(cache, P), dev)
     elif workspace.device != dev:
         raise ValueError(f"workspace must be on {dev}, got {workspace.device}")
-    _run(dev, lib.ri_token_attend, "ri_token_attend", cache._ref, q_ptr, cp, out.data_ptr(),
-         lse.data_ptr(), 1 if add_weight else 0, workspace.data_ptr(), workspace.numel())
+    _run(dev, fn, where, cache._ref, q_ptr, cp, out.data_ptr(), lse.data_ptr(),
+         1 if add_weight else 0, workspace.data_ptr(), workspace.numel(), *test)
     return out, lse
 
 

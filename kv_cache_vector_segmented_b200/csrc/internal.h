@@ -226,7 +226,10 @@ struct TokenAttendArgs {
   float* lse;
   bool add_weight;
   char* ws;
+  unsigned long long wait_ns;  // limit of the device's waits
+  int hand_off;                // self-test: one of these left undone (0: nothing)
 };
+enum { RI_TOKEN_WAIT_TILE = 1, RI_TOKEN_WAIT_SCORES = 2 };
 // Workspace of ri_token_attend in bytes.
 size_t token_attend_bytes(const ri_token_cache& c, int prefix_len);
 cudaError_t launch_token_attend(const TokenAttendArgs& a, cudaStream_t s);

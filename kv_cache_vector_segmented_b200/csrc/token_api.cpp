@@ -73,6 +73,47 @@ bool same_or_apart(const void* a, size_t na, const void* b, size_t nb) {
   return x + na <= y || y + nb <= x;
 }
 
+// ri_token_attend; `hand_off` and `wait_ns` as its self-test sets them.
+ri_status token_attend(const ri_token_cache* cache, const void* q, const ri_token_prefix* prefix,
+                       void* out, float* lse, int32_t add_weight, void* workspace,
+                       size_t workspace_bytes, int hand_off, unsigned long long wait_ns,
+                       ri_stream_t stream) {
+  ri_status st = check_arrays(cache, "token cache");
+  if (st != RI_OK) return st;
+  RI_CHECK(q && aligned16(q) && out && aligned16(out), RI_ERR_INVALID_ARG,
+           "q and out must be non-NULL and 16-byte aligned");
+  RI_CHECK(!lse || aligned4(lse), RI_ERR_INVALID_ARG, "lse must be 4-byte aligned");
+  TokenAttendArgs a = {};
+  if (prefix && prefix->length != 0) {
+    RI_CHECK(prefix->length > 0 && prefix->length <= 1 << 28, RI_ERR_INVALID_ARG,
+             "prefix length must be in [0, 2^28] (got %d)", prefix->length);
+    RI_CHECK(prefix->K && aligned16(prefix->K) && prefix->V && aligned16(prefix->V),
+             RI_ERR_INVALID_ARG, "prefix K and V must be non-NULL and 16-byte aligned");
+    RI_CHECK(prefix->reserved == 0, RI_ERR_INVALID_ARG, "prefix: reserved must be 0");
+    RI_CHECK(prefix->stride_t >= 128 && prefix->stride_t % 8 == 0 &&
+                 (cache->num_kv_heads == 1 ||
+                  (prefix->stride_h >= 128 && prefix->stride_h % 8 == 0)),
+             RI_ERR_INVALID_ARG,
+             "prefix strides must be multiples of 8 elements and at least 128");
+    a.p = *prefix;
+    if (cache->num_kv_heads == 1) a.p.stride_h = a.p.stride_t;
+  }
+  const size_t need = token_attend_bytes(*cache, a.p.length);
+  RI_CHECK(need, RI_ERR_UNSUPPORTED, "prefix of %d tokens: too much work for one call",
+           a.p.length);
+  if ((st = check_workspace(workspace, workspace_bytes, need)) != RI_OK) return st;
+  a.c = *cache;
+  a.q = q;
+  a.out = out;
+  a.lse = lse;
+  a.add_weight = add_weight != 0;
+  a.ws = static_cast<char*>(workspace);
+  a.wait_ns = wait_ns;
+  a.hand_off = hand_off;
+  const cudaError_t e = launch_token_attend(a, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? RI_OK : cuda_fail(e, "token attend launch");
+}
+
 }  // namespace
 
 extern "C" {
@@ -225,38 +266,22 @@ ri_status ri_token_attend(const ri_token_cache* cache, const void* q,
                           const ri_token_prefix* prefix, void* out, float* lse,
                           int32_t add_weight, void* workspace, size_t workspace_bytes,
                           ri_stream_t stream) {
-  ri_status st = check_arrays(cache, "token cache");
-  if (st != RI_OK) return st;
-  RI_CHECK(q && aligned16(q) && out && aligned16(out), RI_ERR_INVALID_ARG,
-           "q and out must be non-NULL and 16-byte aligned");
-  RI_CHECK(!lse || aligned4(lse), RI_ERR_INVALID_ARG, "lse must be 4-byte aligned");
-  TokenAttendArgs a = {};
-  if (prefix && prefix->length != 0) {
-    RI_CHECK(prefix->length > 0 && prefix->length <= 1 << 28, RI_ERR_INVALID_ARG,
-             "prefix length must be in [0, 2^28] (got %d)", prefix->length);
-    RI_CHECK(prefix->K && aligned16(prefix->K) && prefix->V && aligned16(prefix->V),
-             RI_ERR_INVALID_ARG, "prefix K and V must be non-NULL and 16-byte aligned");
-    RI_CHECK(prefix->reserved == 0, RI_ERR_INVALID_ARG, "prefix: reserved must be 0");
-    RI_CHECK(prefix->stride_t >= 128 && prefix->stride_t % 8 == 0 &&
-                 (cache->num_kv_heads == 1 ||
-                  (prefix->stride_h >= 128 && prefix->stride_h % 8 == 0)),
-             RI_ERR_INVALID_ARG,
-             "prefix strides must be multiples of 8 elements and at least 128");
-    a.p = *prefix;
-    if (cache->num_kv_heads == 1) a.p.stride_h = a.p.stride_t;
-  }
-  const size_t need = token_attend_bytes(*cache, a.p.length);
-  RI_CHECK(need, RI_ERR_UNSUPPORTED, "prefix of %d tokens: too much work for one call",
-           a.p.length);
-  if ((st = check_workspace(workspace, workspace_bytes, need)) != RI_OK) return st;
-  a.c = *cache;
-  a.q = q;
-  a.out = out;
-  a.lse = lse;
-  a.add_weight = add_weight != 0;
-  a.ws = static_cast<char*>(workspace);
-  const cudaError_t e = launch_token_attend(a, reinterpret_cast<cudaStream_t>(stream));
-  return e == cudaSuccess ? RI_OK : cuda_fail(e, "token attend launch");
+  return token_attend(cache, q, prefix, out, lse, add_weight, workspace, workspace_bytes, 0,
+                      kWaitLimitNsHost, stream);
+}
+
+ri_status ri_selftest_token_attend_timeout(const ri_token_cache* cache, const void* q,
+                                           const ri_token_prefix* prefix, void* out, float* lse,
+                                           int32_t add_weight, void* workspace,
+                                           size_t workspace_bytes, int32_t hand_off,
+                                           uint64_t limit_ns, ri_stream_t stream) {
+  RI_CHECK(prefix && prefix->length > 0, RI_ERR_INVALID_ARG, "the self-test needs a prefix");
+  RI_CHECK(hand_off == RI_TOKEN_WAIT_TILE || hand_off == RI_TOKEN_WAIT_SCORES, RI_ERR_INVALID_ARG,
+           "hand_off must be 1 or 2 (got %d)", hand_off);
+  RI_CHECK(limit_ns > 0 && limit_ns <= 10ull * 1000000000ull, RI_ERR_INVALID_ARG,
+           "limit_ns must be in (0, 10 s]");
+  return token_attend(cache, q, prefix, out, lse, add_weight, workspace, workspace_bytes, hand_off,
+                      limit_ns, stream);
 }
 
 size_t ri_token_evict_workspace(const ri_token_cache* cache, int32_t budget) {

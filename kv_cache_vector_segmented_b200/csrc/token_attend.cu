@@ -180,6 +180,8 @@ struct AttendParams {
   int* next_task;  // own tasks taken, in the workspace's status region; 0 between calls
   int tasks;       // own tasks: units * splits
   int splits, add_weight;
+  unsigned long long wait_ns;  // limit of a wait in the prefix kernel
+  int hand_off;    // self-test: what the prefix's first block leaves undone (0: nothing)
 };
 
 __device__ __forceinline__ float exp2_approx(float x) {
@@ -555,6 +557,13 @@ struct Share {
   bool pair;
 };
 
+// In the place of a share that a wait's expiry left incomplete (whatever its
+// numerators hold).  Joined with any other, its reference is the greatest, so
+// the sums are l = -inf, which no true share has, and r = NaN: out is NaN.
+__device__ __forceinline__ float4 lost_share() {
+  return make_float4(-kLowest, -INFINITY, __int_as_float(0x7fffffff), 0.f);
+}
+
 template <int kQTiles>
 __device__ __forceinline__ Share share_of(const PrefixPlan& p, int u, int x0, int x1) {
   Share s;
@@ -616,9 +625,11 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
   const int x0 = plan.from(blockIdx.x), x1 = plan.from(blockIdx.x + 1);
   const int u0 = plan.unit_of(x0);
   const int last_tile = plan.key_tiles - 1;
-  // A wait that expires is recorded once; its role then runs on without
-  // waiting, copying or multiplying, so every loop and barrier still ends.
+  // A wait that expires is recorded; its role then runs on without waiting,
+  // copying or multiplying, so every loop and barrier still ends, and the
+  // softmax warps give their shares out as lost ones.
   bool ok = true;
+  auto withheld = [&](int hand_off) { return p.hand_off == hand_off && blockIdx.x == 0; };
 
   if (warp >= kSoftmaxWarps) {
     // one instruction for the whole warpgroup
@@ -631,7 +642,9 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
         tma_prefetch_desc(&map_v);
         auto load = [&](const CUtensorMap* map, int t, int head) {
           const int st = n % kRing;
-          if (ok && n >= kRing && !mbar_wait(&sh->empty[st], (uint32_t)((n / kRing - 1) & 1))) {
+          if (n == 1 && withheld(RI_TOKEN_WAIT_TILE)) ok = false;
+          if (ok && n >= kRing &&
+              !mbar_wait(&sh->empty[st], (uint32_t)((n / kRing - 1) & 1), p.wait_ns)) {
             record_status(p.status, RI_ERR_TIMEOUT);
             ok = false;
           }
@@ -670,7 +683,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
         uint32_t q_phase = 0, p_phases = 0;  // bit i of p_phases: slot i
         auto wait = [&](uint64_t* bar, uint32_t parity) {
           if (ok) {
-            ok = __all_sync(~0u, mbar_wait(bar, parity));
+            ok = __all_sync(~0u, mbar_wait(bar, parity, p.wait_ns));
             if (!ok && lane == 0) record_status(p.status, RI_ERR_TIMEOUT);
           }
         };
@@ -691,7 +704,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
               const uint32_t off = ((k >> 2) * kHalfTile + (k & 3) * 32) >> 4;
               umma_bf16(d, a + off, b + off, idesc_s, k > 0);
             }
-            umma_commit(&sh->s_full[slot]);
+            if (!withheld(RI_TOKEN_WAIT_SCORES)) umma_commit(&sh->s_full[slot]);
           }
           __syncwarp();
         };
@@ -791,7 +804,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
     uint32_t s_phase = 0, o_phase = 0, unit_phase = 0;  // unit: of o_full[0]
     const int H = p.c.num_kv_heads, G = p.c.group_size;
     auto wait = [&](uint64_t* bar, uint32_t parity) {
-      if (ok) ok = __all_sync(~0u, mbar_wait(bar, parity));
+      if (ok) ok = __all_sync(~0u, mbar_wait(bar, parity, p.wait_ns));
       if (!ok && lane == 0) record_status(p.status, RI_ERR_TIMEOUT);
     };
     for (int u = u0; u < plan.units && plan.start(u) < x1; ++u) {
@@ -937,7 +950,13 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
       if (used) {
         wait(&sh->o_full[slot], o_phase);
         o_phase ^= 1;
+      } else {
+        // the other slot's products read the query tile, which the share goes over
+        wait(&sh->o_full[0], unit_phase);
       }
+      const float4 mine = !ok    ? lost_share()
+                          : used ? make_float4(m, l, rs, 0.f)
+                                 : make_float4(-INFINITY, 0.f, 0.f, 0.f);
       // Through shared memory (the query tiles are free: an equal part per
       // warp), so that rows leave as whole 128- or 256-byte pieces: a thread
       // holds a row, and 32 rows' 16-byte stores would each touch 32 lines.
@@ -963,9 +982,9 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
       };
       if (s.pair) {
         named_barrier(1, kSoftmaxWarps * 32);  // both slots' scores are through
-        if (ok && live) {
+        if (live) {
           tc_fence_after();
-          if (lane < n_rows) ml[row] = make_float4(m, l, rs, 0.f);
+          if (lane < n_rows) ml[row] = mine;
 #pragma unroll 1
           for (int c = 0; c < 4; ++c) {
             uint32_t a[32];
@@ -982,19 +1001,15 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
       } else {
         // both slots hold the same rows: (m, l, r) change hands, and each
         // warpgroup joins half of the columns of both numerators
-        // (a slot without a tile waits for the other's products, which read
-        // the query tile this goes over)
-        if (!used) wait(&sh->o_full[0], unit_phase);
         float4* ex = reinterpret_cast<float4*>(sq);  // [2][128]
-        ex[slot * kTile + row] =
-            used ? make_float4(m, l, rs, 0.f) : make_float4(-INFINITY, 0.f, 0.f, 0.f);
+        ex[slot * kTile + row] = mine;
         named_barrier(1, kSoftmaxWarps * 32);
         const float4 e0 = ex[row], e1 = ex[kTile + row];
         named_barrier(1, kSoftmaxWarps * 32);
         const float M = fmaxf(e0.x, e1.x);
         const float f0 = exp2_approx(e0.x - M), f1 = exp2_approx(e1.x - M);
         const bool both = s.t1 - s.t0 > 1;
-        if (ok && live) {
+        if (live) {
           tc_fence_after();
           if (lane < n_rows && slot == 0)
             ml[row] = make_float4(M, f0 * e0.y + f1 * e1.y, f0 * e0.z + f1 * e1.z, 0.f);
@@ -1133,7 +1148,9 @@ __global__ void __launch_bounds__(kMergeThreads, 4)
       f[i] = f[i] > -INFINITY ? exp2_approx(f[i] - M) : -1.f;  // -1: nothing was written
     if (lane == 0) {
       sh_r[g] = rs;
-      sh_lse[g] = l == 0.f ? -INFINITY : M + log2f(l);  // (a sum of NaN: NaN)
+      // (a sum of NaN: NaN; with a lost share: +inf, so that the row's
+      // probabilities, 2^(score - lse), add nothing to the weights)
+      sh_lse[g] = l == 0.f ? -INFINITY : l == -INFINITY ? INFINITY : M + log2f(l);
       sh_n[g] = n_prefix;
       sh_slot[g] = slot;
     }
@@ -1193,7 +1210,8 @@ __global__ void __launch_bounds__(kMergeThreads, 4)
       const size_t row = (size_t)unit * G + g;
       *reinterpret_cast<uint2*>(p.out + row * kD + lane * 4) =
           make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
-      if (p.lse && lane == 0) p.lse[row] = sh_lse[g] * kLn2;
+      if (p.lse && lane == 0)
+        p.lse[row] = sh_lse[g] < INFINITY ? sh_lse[g] * kLn2 : __int_as_float(0x7fffffff);
     }
   }
   if (i0 >= end) return;
@@ -1305,6 +1323,8 @@ cudaError_t launch_token_attend(const TokenAttendArgs& a, cudaStream_t s) {
   const int units = a.c.batch * a.c.num_kv_heads;
   p.tasks = units * L.splits;
   p.add_weight = a.add_weight;
+  p.wait_ns = a.wait_ns;
+  p.hand_off = a.hand_off;
   cudaError_t e = set_smem_once(5, reinterpret_cast<const void*>(own_kernel), (int)kOwnSmem);
   if (e != cudaSuccess) return e;
   if (p.plan.blocks) {
