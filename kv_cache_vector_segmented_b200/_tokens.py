@@ -4,6 +4,8 @@ ri_rotary* and ri_token_* calls of include/retroinfer.h).
 Argument marshalling only, as in _binding: tensors are checked for device,
 dtype, shape and layout, and the calls run on torch's current stream of the
 tensors' device, made current around the call where it is not.
+
+rotary is differentiable; the cache's calls serve and record no gradient.
 """
 from __future__ import annotations
 
@@ -174,6 +176,32 @@ def _no_overlap(out: torch.Tensor, name: str) -> None:
         raise ValueError(f"{name} must not repeat elements (a stride of 0)")
 
 
+def _wants_grad(*tensors) -> bool:
+    """Whether a result of these tensors would carry a gradient."""
+    for t in tensors:
+        if t is not None and t.requires_grad and torch.is_grad_enabled():
+            return True
+    return False
+
+
+class _Rotary(torch.autograd.Function):
+    """The rotation is linear and orthogonal up to its magnitude: the gradient
+    of its input is the inverse rotation of its output's."""
+
+    @staticmethod
+    def forward(ctx, x, positions, table, inverse):
+        ctx.save_for_backward(positions)
+        ctx.table, ctx.inverse = table, inverse
+        return rotary(x, positions, table, inverse=inverse)
+
+    @staticmethod
+    def backward(ctx, grad):
+        if grad.stride(-1) != 1:
+            grad = grad.contiguous()
+        return rotary(grad, *ctx.saved_tensors, ctx.table, inverse=not ctx.inverse), None, None, \
+            None
+
+
 def rotary(x: torch.Tensor, positions: torch.Tensor, table: RotaryTable,
            out: Optional[torch.Tensor] = None, inverse: bool = False) -> torch.Tensor:
     """Rotary positions (ri_rotary) on heads x [B][T][heads][d] (bf16, fp16 or
@@ -181,11 +209,16 @@ def rotary(x: torch.Tensor, positions: torch.Tensor, table: RotaryTable,
     be x itself, or a tensor or view of x's shape (the transpose of
     [B][heads][T][d], say: the layout build_index takes); a new dense tensor
     when not given.  inverse=True turns back: the backward pass of the
-    rotation on its output's gradient."""
+    rotation on its output's gradient.  Differentiable in x, without `out`."""
     if not isinstance(x, torch.Tensor) or x.dim() != 4:
         raise ValueError("x must be a tensor [batch][tokens][heads][head_dim]")
     if x.dtype not in _DTYPES:
         raise TypeError(f"x must be bfloat16, float16 or float32, got {x.dtype}")
+    if _wants_grad(x, out):
+        if out is not None:
+            raise ValueError("rotary records no gradient with `out`: leave it out, or call under "
+                             "torch.no_grad()")
+        return _Rotary.apply(x, positions, table, inverse)
     dev, shape, dtype = x.device, x.shape, x.dtype
     if out is None:
         out = torch.empty(shape, dtype=dtype, device=dev)

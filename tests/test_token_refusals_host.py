@@ -2,6 +2,7 @@
 import ctypes
 
 import pytest
+import torch
 
 PTR = 1 << 20  # an aligned address that no refused call may touch
 INVALID, WORKSPACE = 1, 3
@@ -33,3 +34,16 @@ def test_wait_selftest_refusals(R, C):
                dict(q=None)):
         assert call(**kw) == INVALID, kw
     assert call(n=need - 1) == WORKSPACE
+
+
+def test_rotary_out_records_no_gradient(R):
+    """With `out` no gradient could be recorded: refused rather than lost."""
+    x = torch.zeros(1, 2, 3, 128)
+    pos = torch.zeros(1, 2, dtype=torch.int32)
+    t = R.RotaryTable.make(128, device="cpu")
+    leaf = x.clone().requires_grad_()
+    for a, out in ((leaf, torch.zeros_like(x)), (x, leaf), (leaf, leaf), (leaf * 1, x)):
+        with pytest.raises(ValueError, match="gradient"):
+            R.rotary(a, pos, t, out=out)
+        with torch.no_grad(), pytest.raises(ValueError, match="CUDA"):  # past the check
+            R.rotary(a, pos, t, out=out)
