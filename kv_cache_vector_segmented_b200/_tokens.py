@@ -139,7 +139,8 @@ class RotaryTable:
 
 
 def _heads(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple, dev) -> CHeads:
-    """A strided [B][T][heads][d] tensor as the C struct; only d must be contiguous."""
+    """A strided [B][T][heads][d] tensor as the C struct; only d must be
+    contiguous.  (The stride of an extent of one says nothing: it is passed as 0.)"""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != dtype:
@@ -151,7 +152,8 @@ def _heads(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple, dev) ->
     sb, st, sh, sd = t.stride()
     if sd != 1:
         raise ValueError(f"{name}: the head dimension must be contiguous")
-    return CHeads(t.data_ptr(), sb, st, sh)
+    B, T, H, _ = shape
+    return CHeads(t.data_ptr(), sb if B > 1 else 0, st if T > 1 else 0, sh if H > 1 else 0)
 
 
 def _positions(pos: torch.Tensor, B: int, T: int, dev) -> int:
@@ -360,12 +362,14 @@ def _attend(q, cache, prefix, add_weight, out, lse, workspace, fn, where, *test)
             if t.device != dev:
                 raise ValueError(f"{name} must be on {dev}, got {t.device}")
         P = K.shape[1]
-        sh, st, sd = K.stride()
-        if V.shape != K.shape or (P and V.stride() != K.stride()):
+        if V.shape != K.shape:
             raise ValueError("prefix K and V must have equal shapes and strides")
-        if sd != 1 and P:
-            raise ValueError("prefix: the head dimension must be contiguous")
         if P:
+            (sh, st, sd), (vh, vt, vd) = K.stride(), V.stride()
+            if (H > 1 and vh != sh) or (P > 1 and vt != st):
+                raise ValueError("prefix K and V must have equal shapes and strides")
+            if sd != 1 or vd != 1:
+                raise ValueError("prefix: the head dimension must be contiguous")
             if P == 1:
                 st = d
             cp = ctypes.byref(CTokenPrefix(K.data_ptr(), V.data_ptr(), P, 0, st, sh))
