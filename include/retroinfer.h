@@ -703,7 +703,9 @@ size_t ri_token_evict_workspace(const ri_token_cache* cache, int32_t budget);
 /* Reduces every (sequence, KV head) to keep = min(lens, budget) tokens: first
  * those at positions < keep_first and those at positions > newest -
  * keep_recent (newest: the largest stored position), then the ones of
- * largest weight, ties to the lower row; a NaN weight counts as -inf.  Kept
+ * largest weight, ties to the lower row; a NaN weight counts as -inf.  Where
+ * the first kind alone is more than the budget (several tokens may share a
+ * position), its lowest rows stay, whatever their weights.  Kept
  * tokens in rows below `keep` stay there; the kept tokens behind fill the
  * rows of the dropped ones, both in row order.  The rows' order is not their
  * positions' order afterwards, which attention does not see.

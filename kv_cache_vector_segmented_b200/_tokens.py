@@ -402,7 +402,8 @@ def token_evict(cache: TokenCache, budget: int, keep_first: int = 4, keep_recent
                 workspace: Optional[torch.Tensor] = None) -> TokenCache:
     """ri_token_evict: reduces every (sequence, KV head) to its `budget` tokens
     of most attention weight, those at positions < keep_first and the
-    keep_recent newest positions before all others; in place, or into `out`
+    keep_recent newest positions before all others (by row, where they alone
+    are more than the budget); in place, or into `out`
     (which may share some of the cache's tensors).  Returns the cache that
     holds the result."""
     dev = cache.device

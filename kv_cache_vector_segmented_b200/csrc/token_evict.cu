@@ -3,7 +3,8 @@
 // row `keep` move into the rows of the dropped ones.
 //
 // The order is total: held tokens (first and most recent positions) before
-// all others, then larger weight, then lower row.  A token's rank is a 32-bit
+// all others, by row among themselves; then larger weight, then lower row.  A
+// token's rank is a 32-bit
 // key (the order-preserving image of its weight, all ones when held).  The
 // keep-th token is found by counting: the keys' range is cut into 1024 equal
 // buckets, the bucket that holds the keep-th key is cut again while it has

@@ -78,3 +78,51 @@ def test_prefix_with_strides_of_one(R):
         for k, v in ((_odd(K, *dims), V), (K, _odd(V, *dims)), (_odd(K, *dims), _odd(V, *dims))):
             got = R.token_attend(q, c, (k, v), add_weight=False)
             assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+NAMES = ("K", "V", "pos", "weight", "lens")
+
+
+@gpu
+@pytest.mark.parametrize("heads,cap,budget", [(4, 300, 90), (4, 300, 400), (2, 9000, 4500)])
+def test_evict_into_any_mix_of_arrays(R, heads, cap, budget):
+    """Every array of the result the cache's own or another: in one launch, with
+    nothing to drop, and with a launch of its own for the moves."""
+    first, recent = 3, 20
+    for apart in itertools.product((False, True), repeat=5):
+        g = torch.Generator().manual_seed(budget)
+        c = R.TokenCache.empty(1, heads, 1, cap, DEV)
+        for t in (c.K, c.V, c.weight):
+            t.copy_(torch.randn(t.shape, generator=g))
+        c.pos.copy_(torch.rand(c.pos.shape, generator=g).argsort(-1))
+        c.lens.copy_(torch.randint(0, cap + 1, (1, heads), generator=g))
+        c.lens[0, 0] = cap
+        before = {n: getattr(c, n).clone() for n in NAMES}
+        other = {n: torch.full_like(before[n], -9) for n in NAMES}
+        out = R.TokenCache(*(other[n] if a else getattr(c, n) for n, a in zip(NAMES, apart)))
+        ws = R.alloc_workspace(R.token_evict_workspace_bytes(c, budget), DEV)
+        R.token_evict(c, budget, first, recent, out=out, workspace=ws)
+        assert R.read_device_status(ws) == 0
+        for h in range(heads):
+            n = int(before["lens"][0, h])
+            src = torch.from_numpy(T.evict(before["pos"][0, h, :n].cpu().numpy(),
+                                           before["weight"][0, h, :n].cpu().numpy(), budget,
+                                           first, recent)).to(DEV)
+            m = len(src)
+            assert int(out.lens[0, h]) == m
+            for name, a in zip(NAMES[:4], apart):
+                got, old = getattr(out, name)[0, h], before[name][0, h]
+                assert torch.equal(got[:m], old[src]), (apart, h, name)
+                assert torch.equal(got[m:], torch.full_like(old[m:], -9) if a else old[m:])
+        for name, a in zip(NAMES, apart):
+            assert not a or torch.equal(getattr(c, name), before[name]), (apart, name)
+
+
+@pytest.mark.parametrize("weights", [[.5, .1, .9, .7, .3], [float("nan")] * 5])
+def test_held_beyond_the_budget_stay_by_row(weights):
+    """Without a GPU, by hand: where more tokens are held than the budget (equal
+    positions, say), the lowest rows of them stay, whatever their weights."""
+    w = np.array(weights)
+    assert T.evict(np.array([7, 7, 7, 7, 7]), w, 2, 0, 1).tolist() == [0, 1]
+    assert T.evict(np.array([9, 0, 9, 1, 9]), w, 2, 2, 0).tolist() == [3, 1]
+    assert T.evict(np.array([9, 0, 9, 1, 9]), w, 3, 2, 1).tolist() == [0, 1, 2]
