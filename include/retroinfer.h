@@ -556,10 +556,12 @@ ri_status ri_gather_shape(int64_t host_copies, int64_t total_copies, int32_t* th
  *    after the other, may share one of the largest size.  No other kind of
  *    call may have used the workspace's status region in between without
  *    leaving it zero.
- *  - Make a first call of each kind on a device before capturing one into a
- *    CUDA graph (kernel attributes are set then).
- *  - Kernels here overlap their set-up with the end of the launch before
- *    them and wait for its completion before their first access. */
+ *  - Make a first call of each kind on a device, at the sizes to come, before
+ *    capturing one into a CUDA graph (kernel attributes are set then).
+ *  - A call reads and writes nothing before all that precedes it on the
+ *    stream is complete (the attention's first launch sets up its barriers and
+ *    tensor memory before that).  A call's later launches start while the one
+ *    before them ends, and read early only what that one has waited for. */
 
 /* A strided tensor of heads [B][T][heads][head_dim], head_dim contiguous;
  * strides in elements (a slice of a projection's output, say, or the transpose

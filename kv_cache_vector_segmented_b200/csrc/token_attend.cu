@@ -23,14 +23,17 @@
 // rounded ones takes out what they are off by in common: a token that holds
 // nearly all weight gives its value.
 // (Summed for every tile, r cost the prefix kernel 7 %; where no key counts
-// for an eighth of its row, the unrounded sum goes into r instead.)
+// for an eighth of its row, the unrounded sum goes into r instead.)  What is left
+// of the prefix's roundings is as much as the output's own: behind a long prefix
+// the output is off from 64 bits by 0.0023 of its norm, of which its rounding
+// to bf16 alone makes 0.0017.  Own tokens alone are off by the latter.
 //
 // What bounds it: up to about 100 query rows per KV head the prefix's bytes,
 // beyond that the tensor cores beside the special function unit (a tile's two
 // products take 1024 cycles of the one, its exponentials 1024 of the other),
 // under the power limit.  Measured: 64 sequences of 4 query heads behind 128K
-// tokens of 8 heads 206-216 us in all (157 us for the prefix alone at 1965 MHz:
-// 0.9 PFLOP/s; tensor pipe active 49 %, special functions 46 %), 16 behind 32K
+// tokens of 8 heads 200-216 us in all (157 us for the prefix alone at 1965 MHz:
+// 0.9 PFLOP/s; tensor pipe active 50 %, special functions 47 %), 16 behind 32K
 // 59-61 us (4.1 TB/s over all three launches; the merge and its start take 10).
 // Not kept: part of the exponentials as polynomials on the FMA pipe (184-204
 // against 177 us for the prefix of the largest case: more instructions, more
@@ -129,8 +132,10 @@ AttendLayout layout(const ri_token_cache& c, const PrefixPlan& pp) {
   const size_t units = (size_t)c.batch * c.num_kv_heads;
   // own shares: tasks for 8 warps per SM, two rounds of them, of 64 tokens or
   // more of a full cache; without a prefix (beside which the rounds run into
-  // one another) up to four, the count whose last round is fullest: 512 heads
-  // of 1.7K tokens 90 us against 94 us
+  // one another) up to four, the count whose last round is fullest, the fewest
+  // of about equal ones.  Against two rounds always: 512 heads of 1.7K tokens 89
+  // us (92), 800 of 1K 83 (88), 128 of 4K 56.5 (59); where the rounds were full
+  // anyhow, 128 heads of 1.5K 30.5 us (29.7).
   const long long warps = 8ll * num_sms(), n = (long long)units;
   long long most = (c.capacity + 63) / 64;
   if (most > kMaxSplits) most = kMaxSplits;

@@ -4,10 +4,9 @@
 //
 // The order is total: held tokens (first and most recent positions) before
 // all others, by row among themselves; then larger weight, then lower row.  A
-// token's rank is a 32-bit
-// key (the order-preserving image of its weight, all ones when held).  The
-// keep-th token is found by counting: the keys' range is cut into 1024 equal
-// buckets, the bucket that holds the keep-th key is cut again while it has
+// token's rank is a 32-bit key (the order-preserving image of its weight, all
+// ones when held).  The keep-th token is found by counting: the keys' range is
+// cut into 1024 equal buckets, the bucket that holds the keep-th key is cut again while it has
 // more than 256 keys (one cut is usual: a float's bits spread the weights over
 // the range by their logarithm), and its keys are then ranked one against the
 // other.  Every step is a count, a prefix sum or a comparison: the result does
@@ -37,7 +36,9 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kMoveThreads = 256;
 constexpr int kRowsInFlight = 8;
 constexpr int kRowsPerThread = 2;
-// rows per unit from which a launch of its own for the moves pays
+// Rows per unit from which a launch of its own for the moves pays: 8 heads of
+// 128K rows to 1024, 2048, 4096, 8192 in one launch 31, 33, 38, 45 us, in two 33,
+// 35, 37, 41.
 constexpr int kApartRows = 2048;
 constexpr int kMaxCluster = 16;
 // rows whose keys and positions a block holds (8 bytes each); a longer slice
@@ -518,7 +519,8 @@ cudaError_t launch_token_evict(const TokenEvictArgs& a, cudaStream_t s) {
   p.listed = p.moved + (size_t)units * W;
   // Blocks per unit: more while a block has over kRowsPerThread rows per thread
   // and the grid is within a block per SM.
-  // (of 8 at most, which any GPC holds twice, unless the slices get too long)
+  // Of 8 at most, unless the slices get too long for shared memory: clusters of
+  // 16 took longer, 128K rows of 1, 4, 8 heads 41, 43, 86 us against 33, 37, 41.
   int cluster = 1;
   while (cluster < 8 && cap > cluster * kRowsPerThread * kThreads &&
          (long long)units * cluster * 2 <= num_sms())
@@ -551,7 +553,9 @@ cudaError_t launch_token_evict(const TokenEvictArgs& a, cudaStream_t s) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   // Where the clusters leave much of the machine idle (8 heads of a 128K
-  // prompt: 64 blocks), a second launch over all of it moves the rows.
+  // prompt: 64 blocks), a second launch over all of it moves the rows.  8K rows
+  // halved, one launch and two: 96 blocks (96 heads) 64 and 57 us, 128 blocks (32,
+  // 64, 128 heads) 28 and 31, 47 and 45, 72 and 68.
   p.apart = units * cluster * 4 < 3 * num_sms() && W > kApartRows;
   e = cudaLaunchKernelEx(&cfg, kernel, p);
   if (e != cudaSuccess || !p.apart) return e;
