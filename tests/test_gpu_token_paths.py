@@ -380,3 +380,16 @@ def test_append_many_sequences(R, n, Tn):
     at = pos[:, None].expand(B, H, Tn).gather(2, src)
     assert torch.equal(c.pos, torch.where(new, at, before["pos"]))
     assert torch.equal(c.weight, torch.where(new, 0.0, before["weight"]))
+
+
+@gpu
+@pytest.mark.parametrize("P", [1, 50, 300, 1000])
+@pytest.mark.parametrize("B,H,G", [(520, 32, 4), (4, 400, 4), (37, 160, 7)])
+def test_attend_many_units(R, B, H, G, P):
+    """More (KV head, pair of row tiles) units than SMs: a block takes several in a
+    row, whole ones and parts, pairs and single ones among them."""
+    c, prefix, q, _ = _random(R, B, H, G, P, 20, None, P)
+    q = q.bfloat16()
+    ws = R.alloc_workspace(R.token_attend_workspace_bytes(c, P), DEV)
+    out, lse, w0 = _call(R, q, c, prefix, ws)
+    _check(R, q, c, prefix, out, lse, w0)
