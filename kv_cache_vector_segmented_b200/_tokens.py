@@ -138,17 +138,20 @@ class RotaryTable:
         return cls(turns.to(device), mag.value, interleaved, freq)
 
 
-def _heads(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple, dev) -> CHeads:
+def _heads(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple, dev,
+           measure: bool = False) -> CHeads:
     """A strided [B][T][heads][d] tensor as the C struct; only d must be
-    contiguous.  (The stride of an extent of one says nothing: it is passed as 0.)"""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.device != dev:
-        raise ValueError(f"{name} must be on {dev}, got {t.device}")
+    contiguous.  (The stride of an extent of one says nothing: it is passed as 0.)
+    `measure`: dtype, shape and dev are the tensor's own."""
+    if not measure:
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if t.dtype != dtype:
+            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+        if t.shape != shape:
+            raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+        if t.device != dev:
+            raise ValueError(f"{name} must be on {dev}, got {t.device}")
     sb, st, sh, sd = t.stride()
     if sd != 1:
         raise ValueError(f"{name}: the head dimension must be contiguous")
@@ -176,14 +179,6 @@ def _no_overlap(out: torch.Tensor, name: str) -> None:
     """A written tensor addresses every element once (no stride-0 views)."""
     if 0 in out.stride() and any(s == 0 and n > 1 for s, n in zip(out.stride(), out.shape)):
         raise ValueError(f"{name} must not repeat elements (a stride of 0)")
-
-
-def _wants_grad(*tensors) -> bool:
-    """Whether a result of these tensors would carry a gradient."""
-    for t in tensors:
-        if t is not None and t.requires_grad and torch.is_grad_enabled():
-            return True
-    return False
 
 
 class _Rotary(torch.autograd.Function):
@@ -216,7 +211,7 @@ def rotary(x: torch.Tensor, positions: torch.Tensor, table: RotaryTable,
         raise ValueError("x must be a tensor [batch][tokens][heads][head_dim]")
     if x.dtype not in _DTYPES:
         raise TypeError(f"x must be bfloat16, float16 or float32, got {x.dtype}")
-    if _wants_grad(x, out):
+    if (x.requires_grad or (out is not None and out.requires_grad)) and torch.is_grad_enabled():
         if out is not None:
             raise ValueError("rotary records no gradient with `out`: leave it out, or call under "
                              "torch.no_grad()")
@@ -224,7 +219,7 @@ def rotary(x: torch.Tensor, positions: torch.Tensor, table: RotaryTable,
     dev, shape, dtype = x.device, x.shape, x.dtype
     if out is None:
         out = torch.empty(shape, dtype=dtype, device=dev)
-    cx = _heads(x, "x", dtype, shape, dev)
+    cx = _heads(x, "x", dtype, shape, dev, measure=True)
     co = _heads(out, "out", dtype, shape, dev)
     _no_overlap(out, "out")
     B, T, H, d = shape
@@ -233,7 +228,7 @@ def rotary(x: torch.Tensor, positions: torch.Tensor, table: RotaryTable,
         raise ValueError(f"table must be on {dev}, got {table.turns.device}")
     if x.numel() == 0:
         return out
-    _run(dev, lib.ri_rotary, "ri_rotary", B, T, H, d, _DTYPES[x.dtype], ctypes.byref(cx),
+    _run(dev, lib.ri_rotary, "ri_rotary", B, T, H, d, _DTYPES[dtype], ctypes.byref(cx),
          positions.data_ptr(), sb, table._ref, ctypes.byref(co), 1 if inverse else 0)
     return out
 
